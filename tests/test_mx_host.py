@@ -1,0 +1,109 @@
+"""Host-side tests of the MXFP4 calls (no GPU, no kernel launched): the
+library exports what include/zdo_mx.h declares, the plan's storage equals the
+oracle's, every refusal gives its error code (a build of the host code with
+AddressSanitizer and UndefinedBehaviorSanitizer, tests/host/mx_driver.cpp),
+and the binding's own checks."""
+
+import os
+import re
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+import oracle.layout as OL
+import oracle.mx as MX
+import workloads as W
+import zero_distributed_optimizer_amd as Z
+from zero_distributed_optimizer_amd import mx as ZM
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "zero_distributed_optimizer_amd", "csrc")
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "zdo_mx.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"^\s*[A-Za-z_][\w\s\*]*?\b([a-z_][a-z0-9_]*)\s*\(", text, flags=re.M)))
+    assert len(names) == 9 and sorted(ZM.MX_EXPORTS) == names
+    L = Z.require_library()
+    for n in names:
+        assert hasattr(L, n), n
+        if not n.startswith("zdo_plan"):
+            assert callable(getattr(Z, n))
+
+
+@pytest.mark.parametrize("name", ["tiny", "gpt2_small", "llama3_8b", "llama3_70b", "frag"])
+def test_storage_matches_oracle(name):
+    w = W.get(name)
+    lay = OL.build_layout(w.param_numel, w.bucket_numel, w.dp_size)
+    for rank in (0, w.dp_size - 1):
+        plan = Z.build_range_map(w.param_numel, w.bucket_numel, w.dp_size, rank)
+        for c in (Z.WORLD, Z.LOCAL):
+            assert plan.mx_blocks(c) == MX.storage_blocks(lay, c)
+        want = [(r[5].start, r[5].stop - r[5].start) for r in MX.ranges(lay, rank)]
+        assert [tuple(map(int, x)) for x in plan.mx_buckets()] == want
+        assert plan.norm_mxfp4_workspace_bytes == 8 * (plan.mx_blocks(Z.LOCAL) // 16 + 1024)
+        plan.destroy()
+
+
+def test_checks_and_storage_under_host_sanitizers(tmp_path):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not available")
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("runs on a host without a GPU (the plans must stay host-only)")
+    exe = str(tmp_path / "mx_driver")
+    cmd = [hipcc, "-x", "hip", "--offload-arch=gfx950", "-O1", "-g", "-std=c++17",
+           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
+           os.path.join(ROOT, "tests", "host", "mx_driver.cpp"),
+           *[os.path.join(CSRC, f) for f in ("plan.cpp", "abi.cpp", "mx_abi.cpp")], "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True, cwd=str(tmp_path))
+    assert r.returncode == 0, r.stderr[-3000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0", UBSAN_OPTIONS="print_stacktrace=1")
+    r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=600)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+    assert "ok: storage of 2000 plans" in r.stdout
+
+
+def test_binding_refuses_before_the_library():
+    import torch
+    plan = Z.build_range_map([1000, 24], 600, 4, 1)
+    host = torch.zeros(4096, dtype=torch.int16)
+    with pytest.raises(ValueError, match="device"):
+        Z.quantize_grads_mxfp4(plan, host, Z.WORLD, None)
+    with pytest.raises(TypeError, match="torch tensor"):
+        Z.MxBuffers([(np.zeros(16, np.uint8), np.zeros(1, np.uint8))])
+    with pytest.raises(ValueError, match="device"):
+        Z.MxBuffers([(torch.zeros(16, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8))])
+    with pytest.raises(ValueError, match="coords"):
+        plan.mx_blocks(2)
+    assert len(Z.MxBuffers([])) == 0
+    c, s = Z.mx_empty(plan, Z.LOCAL, "cpu")
+    assert c.shape == (plan.mx_blocks(Z.LOCAL), 16) and s.shape == (plan.mx_blocks(Z.LOCAL),)
+    assert not c.any() and not s.any()
+
+
+def test_calls_on_a_host_only_plan_are_errors():
+    import ctypes
+
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    L = Z.require_library()
+    plan = Z.build_range_map([10, 20], 16, 2, 0)
+    two = (ctypes.c_void_p * 2)(1 << 20, 1 << 21)
+    hp = Z.adam_hparams(1e-3, 0.9, 0.999, 1e-8, 0.0, 1)
+    h = plan.handle
+    assert L.quantize_grads_mxfp4(h, 0, 1, 16, 0, None, 32, 48, None) == Z.EHIP
+    assert L.reduce_scatter_local_mxfp4(h, 0, 1, two, two, 2, 0, 1.0, 16, 0, None) == Z.EHIP
+    assert L.grad_norm_sq_mxfp4(h, two, two, 2, 0, 1.0, 16, 32, None) == Z.EHIP
+    assert L.sharded_adam_step_mxfp4(h, 0, 1, two, two, 2, 0, 1.0, 16, 32, 48, None, 0, None, None, 0,
+                                     ctypes.byref(hp), None, None, None) == Z.EHIP
+    assert L.writeback_params_mxfp4(h, 16, 32, 48, 0, None) == Z.EHIP
+    assert L.all_gather_params_mxfp4(h, two, two, 2, 0, 16, None) == Z.EHIP
+    assert b"device" in L.zdo_last_error()

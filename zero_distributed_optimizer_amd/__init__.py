@@ -10,6 +10,9 @@ implementation.
     plan = build_range_map(param_numel, bucket_numel, dp_size, rank)
     sharded_adam_step(plan, replicas, WORLD, scale, master, exp_avg, exp_avg_sq,
                       param_buffer, WORLD, lr=..., beta1=..., ..., step=t)
+
+The calls with contributions and parameters in 4 bits (include/zdo_mx.h) are in
+mx.py and reached from here as well.
 """
 
 from __future__ import annotations
@@ -139,6 +142,7 @@ def require_library() -> ctypes.CDLL:
               "sharded_adam_step_instances", "all_gather_params", "zdo_device_copy",
               "reduce_scatter_local_bucket_list", "sharded_adam_step_bucket_list", "zdo_stream_probe"):
         getattr(L, f).restype = ctypes.c_int
+    mx.declare(L)
     _lib = L
     return L
 
@@ -184,6 +188,9 @@ class Plan:
         self.buffer_numel = int(L.zdo_plan_buffer_numel(h))
         self.shard_numel = int(L.zdo_plan_shard_numel(h))
         self.owned_numel = int(L.zdo_plan_owned_numel(h))
+        n = ctypes.c_int32()
+        _check(L.zdo_plan_buckets(h, None, 0, ctypes.byref(n)))
+        self.num_buckets = int(n.value)
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -210,6 +217,26 @@ class Plan:
     @property
     def norm_workspace_bytes(self) -> int:
         return int(require_library().zdo_plan_norm_workspace_bytes(self.handle))
+
+    @property
+    def norm_mxfp4_workspace_bytes(self) -> int:
+        return int(require_library().zdo_plan_norm_mxfp4_workspace_bytes(self.handle))
+
+    def mx_blocks(self, coords: int) -> int:
+        """Blocks of the plan's MXFP4 storage in WORLD or LOCAL coordinates."""
+        n = int(require_library().zdo_plan_mx_blocks(self.handle, coords))
+        if n < 0:
+            raise ValueError("coords must be WORLD or LOCAL")
+        return n
+
+    def mx_buckets(self) -> np.ndarray:
+        """Per bucket, its first block and its blocks in LOCAL storage (include/zdo_mx.h)."""
+        L = require_library()
+        n = ctypes.c_int32()
+        _check(L.zdo_plan_mx_buckets(self.handle, None, 0, ctypes.byref(n)))
+        out = np.zeros(n.value, dtype=mx.MX_BUCKET_DTYPE)
+        _check(L.zdo_plan_mx_buckets(self.handle, out.ctypes.data, n.value, ctypes.byref(n)))
+        return out
 
     def extent(self, coords: int) -> int:
         return self.buffer_numel if coords == WORLD else self.shard_numel
@@ -479,3 +506,8 @@ def stream_probe(reads, state, out, n: int, waves_per_cu: int = 0, stream=None, 
     o = _dev_ptr(out, "out", "bf16", n)
     _check(require_library().zdo_stream_probe(r, len(reads), s0, s1, s2, o, n, stores, waves_per_cu,
                                               _stream(stream, out.device)))
+
+
+from . import mx  # noqa: E402  (it uses the names above)
+from .mx import (MxBuffers, all_gather_params_mxfp4, grad_norm_sq_mxfp4, mx_empty,  # noqa: E402,F401
+                 quantize_grads_mxfp4, reduce_scatter_local_mxfp4, sharded_adam_step_mxfp4, writeback_params_mxfp4)

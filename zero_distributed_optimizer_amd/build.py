@@ -23,8 +23,8 @@ LIB = os.path.join(HERE, "libzdo.so")
 # build only launches of more than 2^24 tiles do).
 GRID_LOOP_LIB = os.path.join(HERE, "libzdo_gridloop.so")
 GRID_LOOP_FLAGS = ["-DZDO_MAX_GRID=64"]
-SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip"]
-HEADERS = ["zdo_internal.h", "kernels.h"]
+SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "mx_abi.cpp", "mx_kernels.hip"]
+HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -38,7 +38,7 @@ FLAGS = [
 
 def sources() -> list[str]:
     return [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS] + \
-        [os.path.join(INCLUDE, "zdo.h")]
+        [os.path.join(INCLUDE, "zdo.h"), os.path.join(INCLUDE, "zdo_mx.h")]
 
 
 def build(verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:

@@ -9,6 +9,7 @@
 #include <utility>
 #include <vector>
 
+#include "checks.h"
 #include "kernels.h"
 #include "zdo_internal.h"
 
@@ -21,63 +22,6 @@ int upload_plan(zdo_plan &p);
 namespace {
 
 thread_local std::string g_error;
-
-struct Span {
-    uintptr_t lo, hi;
-};
-
-Span span_of(const void *p, int64_t elems, int64_t elem_bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + uintptr_t(elems) * uintptr_t(elem_bytes)};
-}
-
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int fail(int code, const std::string &msg) {
-    g_error = msg;
-    return code;
-}
-
-// The plan must be device-ready, and on the current device.
-int check_plan(const zdo_plan *plan, const char *fn) {
-    if (!plan)
-        return fail(ZDO_EINVAL, std::string(fn) + ": plan is NULL");
-    if (!plan->d_table)
-        return fail(ZDO_EHIP, std::string(fn) + ": the plan has no device table (no HIP device when it was built)");
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess)
-        return fail(ZDO_EHIP, std::string(fn) + ": hipGetDevice failed");
-    if (dev != plan->device)
-        return fail(ZDO_EINVAL, std::string(fn) + ": the plan was built on device " + std::to_string(plan->device) +
-                                    " but device " + std::to_string(dev) + " is current");
-    return ZDO_OK;
-}
-
-int check_coords(int32_t c, const char *fn, const char *what) {
-    if (c != ZDO_WORLD && c != ZDO_LOCAL)
-        return fail(ZDO_EINVAL, std::string(fn) + ": " + what + " must be ZDO_WORLD or ZDO_LOCAL");
-    return ZDO_OK;
-}
-
-int check_ptr(const void *p, const char *fn, const char *what) {
-    if (!p)
-        return fail(ZDO_EINVAL, std::string(fn) + ": " + what + " is NULL");
-    if (!aligned16(p))
-        return fail(ZDO_EALIGN, std::string(fn) + ": " + what + " is not 16-byte aligned");
-    return ZDO_OK;
-}
-
-int64_t extent(const zdo_plan *p, int32_t coords) { return coords == ZDO_WORLD ? p->buffer_numel : p->shard_numel; }
-
-int launch_result(hipError_t e, const char *fn) {
-    if (e != hipSuccess)
-        return fail(ZDO_EHIP, std::string(fn) + ": launch failed: " + hipGetErrorString(e));
-    return ZDO_OK;
-}
 
 // Checks the replica list; fills `rep`.
 int take_replicas(const zdo_plan *p, const uint16_t *const *replicas, int32_t n, int32_t coords, const char *fn,
@@ -92,37 +36,6 @@ int take_replicas(const zdo_plan *p, const uint16_t *const *replicas, int32_t n,
         spans[j] = span_of(replicas[j], extent(p, coords), 2);
     }
     return ZDO_OK;
-}
-
-// 1 - beta^t: the double 1.0 multiplied t times by (double)beta, rounded once
-// to fp32 (beta in [0, 1)). Once beta^t < 2^-60, 1 - beta^t is 1.0 in double
-// and stays so for every larger t, so the products stop there. The last
-// (beta, t, product) of a few betas is kept per thread, so that consecutive
-// steps cost O(1).
-float bias_correction(float beta, int64_t t) {
-    struct Entry {
-        float beta;
-        int64_t t;
-        double pw;
-    };
-    thread_local Entry cache[4] = {{-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}};
-    thread_local unsigned next = 0;
-    Entry *e = nullptr;
-    for (auto &c : cache)
-        if (c.beta == beta && c.t <= t)
-            e = &c;
-    double pw = 1.0;
-    int64_t i = 0;
-    if (e) {
-        pw = e->pw;
-        i = e->t;
-    } else {
-        e = &cache[next++ % 4];
-    }
-    for (; i < t && pw >= 0x1p-60; ++i)
-        pw *= double(beta);
-    *e = {beta, t, pw};
-    return float(1.0 - pw);
 }
 
 // Tiles [first, first + count) of a launch space that cover buckets [b0, b1):
@@ -143,13 +56,6 @@ void bucket_tiles(const std::vector<Seg> &segs, const int32_t *seg_bucket, int64
     };
     first = first_seg_at(b0);
     count = first_seg_at(b1) - first;
-}
-
-int check_buckets(const zdo_plan *plan, int32_t b0, int32_t b1, const char *fn) {
-    if (b0 < 0 || b1 < b0 || b1 > int32_t(plan->buckets.size()))
-        return fail(ZDO_EINVAL, std::string(fn) + ": need 0 <= bucket_begin <= bucket_end <= " +
-                                    std::to_string(plan->buckets.size()));
-    return ZDO_OK;
 }
 
 typedef std::pair<int32_t, int32_t> BucketRange;
@@ -228,6 +134,61 @@ int launch_runs(const std::vector<TileRun> &runs, const Seg *segs, const GroupSe
 }  // namespace
 
 void set_error(const std::string &msg) { g_error = msg; }
+
+// 1 - beta^t: the double 1.0 multiplied t times by (double)beta, rounded once
+// to fp32 (beta in [0, 1)). Once beta^t < 2^-60, 1 - beta^t is 1.0 in double
+// and stays so for every larger t, so the products stop there. The last
+// (beta, t, product) of a few betas is kept per thread, so that consecutive
+// steps cost O(1).
+static float bias_correction(float beta, int64_t t) {
+    struct Entry {
+        float beta;
+        int64_t t;
+        double pw;
+    };
+    thread_local Entry cache[4] = {{-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}, {-1.0f, 0, 1.0}};
+    thread_local unsigned next = 0;
+    Entry *e = nullptr;
+    for (auto &c : cache)
+        if (c.beta == beta && c.t <= t)
+            e = &c;
+    double pw = 1.0;
+    int64_t i = 0;
+    if (e) {
+        pw = e->pw;
+        i = e->t;
+    } else {
+        e = &cache[next++ % 4];
+    }
+    for (; i < t && pw >= 0x1p-60; ++i)
+        pw *= double(beta);
+    *e = {beta, t, pw};
+    return float(1.0 - pw);
+}
+
+int check_adam(const zdo_adam *hp, const char *fn) {
+    if (!hp)
+        return fail(ZDO_EINVAL, std::string(fn) + ": hp is NULL");
+    if (hp->step < 1 || hp->reserved != 0)
+        return fail(ZDO_EINVAL, std::string(fn) + ": hp->step must be >= 1 and hp->reserved 0");
+    if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+        return fail(ZDO_EINVAL, std::string(fn) + ": beta1 and beta2 must be in [0, 1)");
+    return ZDO_OK;
+}
+
+AdamConst adam_const(const zdo_adam &hp) {
+    AdamConst c;
+    c.lr = hp.lr;
+    c.b1 = hp.beta1;
+    c.b2 = hp.beta2;
+    c.omb1 = 1.0f - hp.beta1;
+    c.omb2 = 1.0f - hp.beta2;
+    c.eps = hp.eps;
+    c.wd = hp.weight_decay;
+    c.bc1 = bias_correction(hp.beta1, hp.step);
+    c.bc2 = bias_correction(hp.beta2, hp.step);
+    return c;
+}
 
 }  // namespace zdo
 
@@ -420,12 +381,8 @@ static int adam_step(const char *fn, const zdo_plan *plan, const std::vector<Buc
     if (param_out)
         if (int rc = check_coords(param_coords, fn, "param_coords"))
             return rc;
-    if (!hp)
-        return fail(ZDO_EINVAL, std::string(fn) + ": hp is NULL");
-    if (hp->step < 1 || hp->reserved != 0)
-        return fail(ZDO_EINVAL, std::string(fn) + ": hp->step must be >= 1 and hp->reserved 0");
-    if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
-        return fail(ZDO_EINVAL, std::string(fn) + ": beta1 and beta2 must be in [0, 1)");
+    if (int rc = check_adam(hp, fn))
+        return rc;
     StepArgs a{};
     Span gs[ZDO_MAX_REPLICAS];
     if (int rc = take_replicas(plan, grads, n_grads, grad_coords, fn, a.rep, gs))
@@ -483,15 +440,7 @@ static int adam_step(const char *fn, const zdo_plan *plan, const std::vector<Buc
     a.main_grad = main_grad_out;
     a.coeff = coeff;
     a.state_numel = L;
-    a.c.lr = hp->lr;
-    a.c.b1 = hp->beta1;
-    a.c.b2 = hp->beta2;
-    a.c.omb1 = 1.0f - hp->beta1;
-    a.c.omb2 = 1.0f - hp->beta2;
-    a.c.eps = hp->eps;
-    a.c.wd = hp->weight_decay;
-    a.c.bc1 = bias_correction(hp->beta1, hp->step);
-    a.c.bc2 = bias_correction(hp->beta2, hp->step);
+    a.c = adam_const(*hp);
     const std::vector<TileRun> runs = tile_runs(plan->param_segs, plan->param_seg_bucket.data(), plan->param_tiles,
                                                 ranges);
     return launch_runs(runs, plan->d_param_segs, plan->d_param_group, int64_t(plan->param_segs.size()), fn,

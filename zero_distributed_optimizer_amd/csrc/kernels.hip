@@ -35,6 +35,7 @@
 #include <cstddef>
 #include <mutex>
 
+#include "device.h"
 #include "kernels.h"
 
 #pragma clang fp contract(off)
@@ -50,65 +51,6 @@ static __device__ __align__(256) unsigned char scratch[ZDO_NO_ALLOC_SCRATCH_BYTE
 namespace zdo {
 namespace {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// ---- bf16 ----------------------------------------------------------------------
-// A bf16 is the top half of an fp32: widening is a shift or a mask.
-__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float h_f32(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }
-
-// Two fp32 to their nearest bf16 (ties to even), packed a | b << 16: one
-// v_cvt_pk_bf16_f32 on gfx950.
-__device__ __forceinline__ uint32_t to_bf16x2(float a, float b) {
-    f32x2 v = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
-
-// ---- memory ------------------------------------------------------------------------
-// The replicas are read exactly once per launch: their loads carry the
-// non-temporal hint, which keeps them from displacing the fp32 state in the
-// caches (measured: +2% on a 42 GB step, +18% when the state fits the
-// 256 MB Infinity Cache between steps). The write-only outputs (parameters,
-// reduced gradient, main grad) are non-temporal stores too (Llama-3-8B-shaped
-// step: 6.83 ms in every run against 6.83-7.48 ms with plain stores;
-// Llama-3-70B-shaped reduce-scatter 7% faster). The fp32 state is read and
-// then rewritten. While it is at most a few times the 256 MB Infinity
-// Cache, plain loads and stores serve it best (GPT-2-shaped step, 187 MB of
-// state, back to back: 97.5 us against 109.8 us with non-temporal state
-// accesses). Beyond 1 GiB (see launch_step) the step loads and stores it
-// non-temporally as well (Llama-3-8B-shaped step: 6.92-6.98 -> 6.75-6.77
-// ms); non-temporal stores after plain loads of the same lines are far
-// slower than either (3.4-3.6 TB/s).
-__device__ __forceinline__ u32x4 ld_rep(const uint16_t *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-}
-__device__ __forceinline__ f32x4 ldf4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-__device__ __forceinline__ void st16_out(uint16_t *p, u32x4 v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
-}
-__device__ __forceinline__ void stf4(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
-__device__ __forceinline__ void stf4_out(float *p, f32x4 v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(p));
-}
-template <bool kNT>
-__device__ __forceinline__ f32x4 ld_state(const float *p) {
-    if constexpr (kNT)
-        return __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
-    else
-        return ldf4(p);
-}
-template <bool kNT>
-__device__ __forceinline__ void st_state(float *p, f32x4 v) {
-    if constexpr (kNT)
-        __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(p));
-    else
-        stf4(p, v);
-}
-
 // ---- walking the segments -------------------------------------------------------------
 struct ChunkPos {
     int64_t w0;     // WORLD index of the chunk's first slot (a multiple of 8)
@@ -116,16 +58,6 @@ struct ChunkPos {
     int lo, hi;     // the chunk's slots [lo, hi) that belong to the segment
 };
 
-// The plan's tables are read-only for the life of the plan: read through the
-// constant address space, the compiler fetches them with scalar loads (one
-// per wave, into scalar registers) instead of 64-lane vector loads of one
-// address.
-template <typename T>
-using ro_ptr = const __attribute__((address_space(4))) T *;
-template <typename T>
-__device__ __forceinline__ ro_ptr<T> ro(const T *p) {
-    return (ro_ptr<T>)(p);
-}
 __device__ __forceinline__ Seg ld_seg(ro_ptr<Seg> p) {
     Seg s;
     s.wbeg = p->wbeg;
@@ -285,27 +217,6 @@ __device__ __forceinline__ float reduce_one_instances(const uint16_t *const *rep
     return acc;
 }
 
-// ---- Adam --------------------------------------------------------------------------------------
-__device__ __forceinline__ void adam(const AdamConst &c, float g, float &p, float &m, float &v) {
-    const float m1 = c.b1 * m;
-    const float m2 = c.omb1 * g;
-    const float mn = m1 + m2;
-    const float gg = g * g;
-    const float v1 = c.b2 * v;
-    const float v2 = c.omb2 * gg;
-    const float vn = v1 + v2;
-    const float mh = mn / c.bc1;
-    const float vh = vn / c.bc2;
-    const float den = __builtin_sqrtf(vh) + c.eps;
-    const float u = mh / den;
-    const float wdp = c.wd * p;
-    const float u2 = u + wdp;
-    const float st = c.lr * u2;
-    p = p - st;
-    m = mn;
-    v = vn;
-}
-
 // ---- kernels -------------------------------------------------------------------------------------
 
 template <int D>
@@ -345,8 +256,6 @@ __global__ __launch_bounds__(kBlock) void reduce_kernel(ReduceArgs a) {
 // shards. A lane whose two quads both lie inside the segment issues every
 // load of the tile before any arithmetic; at a segment's edges a full quad
 // goes alone and a partial one slot by slot.
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ u32x2 ld_rep2(const uint16_t *p) {
     return __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
 }
@@ -906,20 +815,6 @@ __global__ __launch_bounds__(kBlock) void copy_kernel(u32x4 *dst, const u32x4 *s
         __builtin_nontemporal_store(__builtin_nontemporal_load(src + i), dst + i);
 }
 
-// Enough blocks to cover every tile once, up to a cap that keeps the grid's
-// work-item count in range; larger launches loop over tiles (every kernel's
-// tile loop steps by gridDim.x). A build with a small cap makes every
-// launch take that loop.
-#ifndef ZDO_MAX_GRID
-#define ZDO_MAX_GRID (int64_t(1) << 24)
-#endif
-constexpr int64_t kMaxGrid = ZDO_MAX_GRID;
-static_assert(kMaxGrid >= 1 && kMaxGrid <= (int64_t(1) << 24), "grid cap out of range");
-
-unsigned grid_for(int64_t ntiles) {
-    return unsigned(ntiles < kMaxGrid ? ntiles : kMaxGrid);
-}
-
 // HBM serves a long stream of many read and write streams at a higher rate
 // when fewer waves share a compute unit (measured on the 42 GB
 // Llama-3-8B-shaped step: 5.32 TB/s uncapped, 5.69 TB/s at 10 waves per
@@ -947,17 +842,6 @@ unsigned grid_for(int64_t ntiles) {
 // 344-345 us at 10, 335-338 at 8, 358-362 at 7) and with 7 at 16
 // (fragmentation workload: 414-415 us at 10, 413-414 at 8, 394-395 at 7).
 constexpr int flat_waves(int nrep) { return nrep >= 16 ? 7 : 8; }
-
-// LDS per workgroup that lets at most `waves` waves share a compute unit.
-unsigned lds_for_waves(int lds_per_cu, int waves) {
-    if (waves <= 0 || lds_per_cu <= 0)
-        return 0;
-    const int waves_per_group = kBlock / 64;
-    int groups = waves / waves_per_group;
-    if (groups < 4 / waves_per_group + (waves_per_group > 4))
-        groups = 4 / waves_per_group + (waves_per_group > 4);
-    return unsigned(lds_per_cu / groups) & ~127u;
-}
 
 unsigned lds_reserve(int lds_per_cu, int64_t ntiles, int long_waves = ZDO_WAVES_PER_CU) {
     return lds_for_waves(lds_per_cu, ntiles < kShortLaunchTiles ? ZDO_WAVES_PER_CU_SHORT : long_waves);
@@ -989,19 +873,6 @@ hipError_t launch_reduce(const ReduceArgs &a, int lds_per_cu, hipStream_t stream
     }
     return hipGetLastError();
 }
-
-// The fp32 state goes non-temporal above 1 GiB (12 bytes per shard slot).
-// Measured on one box, plain -> non-temporal state, step time with cold
-// caches (back to back in brackets): 187 MB 102 -> 112 us (97 -> 109),
-// 299 MB 148 -> 159 us (150 -> 155), 498 MB 209 -> 218 us (235 -> 216),
-// 747 MB 296 -> 308 us (323 -> 307), 1.49 GB 582 -> 562 us (603 -> 565),
-// 3.0 GB 4.09 -> 3.99 ms, 6.0 GB 4.91 -> 4.73 ms, 12 GB 6.96 -> 6.76 ms.
-// Between steps of a training run the caches are cold, and there
-// non-temporal accesses pay off once the state is well beyond the 256 MB
-// Infinity Cache.
-#ifndef ZDO_STATE_CACHE_BYTES
-#define ZDO_STATE_CACHE_BYTES (int64_t(1) << 30)
-#endif
 
 template <bool kNT>
 void launch_step_as(const StepArgs &a, dim3 grid, dim3 block, unsigned lds, hipStream_t stream) {
@@ -1036,7 +907,7 @@ hipError_t launch_step(const StepArgs &a, int lds_per_cu, hipStream_t stream) {
     const int d = a.ninst > 1 && a.dinst > 1 ? a.dinst : a.nrep;   // the template's D
     const bool fixed = d == 2 || d == 4 || d == 8 || d == 16 || d == 32;
     const unsigned lds = lds_reserve(lds_per_cu, a.walk.ntiles, fixed ? ZDO_STEP_WAVES_PER_CU : ZDO_WAVES_PER_CU);
-    if (a.state_numel * int64_t(3 * sizeof(float)) > ZDO_STATE_CACHE_BYTES)
+    if (state_nontemporal(a.state_numel))
         launch_step_as<true>(a, grid, block, lds, stream);
     else
         launch_step_as<false>(a, grid, block, lds, stream);
@@ -1053,10 +924,24 @@ hipError_t launch_writeback(const WritebackArgs &a, hipStream_t stream) {
     // non-temporal on the step's rule (Llama-3-8B uncapped: 1004-1007 us
     // with plain loads; GPT-2: 16.2 us with non-temporal ones).
     const dim3 grid(grid_for(a.walk.ntiles)), block(kBlock);
-    if (a.state_numel * int64_t(3 * sizeof(float)) > ZDO_STATE_CACHE_BYTES)
+    if (state_nontemporal(a.state_numel))
         hipLaunchKernelGGL(writeback_kernel<true>, grid, block, 0, stream, a);
     else
         hipLaunchKernelGGL(writeback_kernel<false>, grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_tile_sums(double *partial, int64_t n, double *norm_sq, hipStream_t stream) {
+    // level 1: G <= kSumGroups runs of `chunk` partials; level 2: one workgroup
+    int64_t g = (n + kSumThreads - 1) / kSumThreads;
+    if (g > kSumGroups)
+        g = kSumGroups;
+    if (g < 1)
+        g = 1;
+    const int64_t chunk = n > 0 ? (n + g - 1) / g : 1;
+    double *level = partial + (n > 0 ? n : 0);
+    hipLaunchKernelGGL(tile_sum_kernel, dim3(unsigned(g)), dim3(kSumThreads), 0, stream, partial, n, chunk, level);
+    hipLaunchKernelGGL(level_sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, level, g, norm_sq);
     return hipGetLastError();
 }
 
@@ -1077,18 +962,7 @@ hipError_t launch_norm(const NormArgs &a, double *norm_sq, int lds_per_cu, hipSt
         if (e != hipSuccess)
             return e;
     }
-    // level 1: G <= kSumGroups runs of `chunk` partials; level 2: one workgroup
-    const int64_t n = a.walk.ntiles;
-    int64_t g = (n + kSumThreads - 1) / kSumThreads;
-    if (g > kSumGroups)
-        g = kSumGroups;
-    if (g < 1)
-        g = 1;
-    const int64_t chunk = n > 0 ? (n + g - 1) / g : 1;
-    double *level = a.partial + (n > 0 ? n : 0);
-    hipLaunchKernelGGL(tile_sum_kernel, dim3(unsigned(g)), dim3(kSumThreads), 0, stream, a.partial, n, chunk, level);
-    hipLaunchKernelGGL(level_sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, level, g, norm_sq);
-    return hipGetLastError();
+    return launch_tile_sums(a.partial, a.walk.ntiles, norm_sq, stream);
 }
 
 namespace {

@@ -140,6 +140,15 @@ int build_plan(const int64_t *param_numel, int32_t n_params, int64_t bucket_nume
             gt += range_tiles(rb, b.shard_numel);
         }
     p.gather_tiles = gt;
+    for (const auto &b : p.buckets) {
+        const int64_t t = mx_range_tiles(b.shard_numel), u = (t + kMxUnit - 1) / kMxUnit;
+        // beyond 32 bits the MXFP4 calls refuse the plan (kMxMaxTiles)
+        const int64_t cap = std::numeric_limits<int32_t>::max();
+        p.mx_buckets.push_back({b.offset, b.numel, b.shard_numel, b.shard_base, p.mx_tiles, p.mx_units,
+                                int32_t(std::min(t, cap)), int32_t(std::min(u, cap))});
+        p.mx_tiles += t;
+        p.mx_units += u;
+    }
     return ZDO_OK;
 }
 
@@ -180,13 +189,22 @@ int upload_plan(zdo_plan &p) {
     const auto range_group = group_segs(p.range_segs, p.range_tiles);
     const auto gather_group =
         group_index(p.gather_tiles, p.gather_ranges.size(), [&](size_t y) { return p.gather_ranges[y].tile0; });
+    // the MXFP4 walks' index; a plan that the MXFP4 calls refuse has none
+    const bool mx = p.mx_tiles <= kMxMaxTiles;
+    const auto mx_tile_group = group_index(mx ? p.mx_tiles : 0, p.mx_buckets.size(),
+                                           [&](size_t y) { return p.mx_buckets[y].tile0; });
+    const auto mx_unit_group = group_index(mx ? p.mx_units : 0, p.mx_buckets.size(),
+                                           [&](size_t y) { return p.mx_buckets[y].unit0; });
     // one allocation: segments, the two walks' group entries, the gather
-    // ranges, then the gather's group index
+    // ranges, the MXFP4 buckets, then the gather's and the MXFP4 walks' index
     const size_t nseg = p.param_segs.size() + p.range_segs.size();
     const size_t seg_bytes = nseg * sizeof(Seg);
     const size_t gseg_bytes = (param_group.size() + range_group.size()) * sizeof(GroupSeg);
     const size_t span_bytes = p.gather_ranges.size() * sizeof(RangeSpan);
-    const size_t bytes = seg_bytes + gseg_bytes + span_bytes + gather_group.size() * sizeof(uint32_t);
+    const size_t mxb_bytes = p.mx_buckets.size() * sizeof(MxBucket);
+    const size_t index_at = seg_bytes + gseg_bytes + span_bytes + mxb_bytes;
+    const size_t bytes =
+        index_at + (gather_group.size() + mx_tile_group.size() + mx_unit_group.size()) * sizeof(uint32_t);
     std::vector<char> host(bytes);
     std::copy(p.param_segs.begin(), p.param_segs.end(), reinterpret_cast<Seg *>(host.data()));
     std::copy(p.range_segs.begin(), p.range_segs.end(),
@@ -196,8 +214,12 @@ int upload_plan(zdo_plan &p) {
     std::copy(range_group.begin(), range_group.end(), gs);
     std::copy(p.gather_ranges.begin(), p.gather_ranges.end(),
               reinterpret_cast<RangeSpan *>(host.data() + seg_bytes + gseg_bytes));
-    std::copy(gather_group.begin(), gather_group.end(),
-              reinterpret_cast<uint32_t *>(host.data() + seg_bytes + gseg_bytes + span_bytes));
+    std::copy(p.mx_buckets.begin(), p.mx_buckets.end(),
+              reinterpret_cast<MxBucket *>(host.data() + seg_bytes + gseg_bytes + span_bytes));
+    uint32_t *gi = reinterpret_cast<uint32_t *>(host.data() + index_at);
+    gi = std::copy(gather_group.begin(), gather_group.end(), gi);
+    gi = std::copy(mx_tile_group.begin(), mx_tile_group.end(), gi);
+    std::copy(mx_unit_group.begin(), mx_unit_group.end(), gi);
     void *d = nullptr;
     hipError_t e = hipMalloc(&d, bytes);
     if (e != hipSuccess) {
@@ -217,8 +239,11 @@ int upload_plan(zdo_plan &p) {
     p.d_param_group = reinterpret_cast<const GroupSeg *>(static_cast<const char *>(d) + seg_bytes);
     p.d_range_group = p.d_param_group + param_group.size();
     p.d_gather_ranges = reinterpret_cast<const RangeSpan *>(static_cast<const char *>(d) + seg_bytes + gseg_bytes);
-    p.d_gather_group =
-        reinterpret_cast<const uint32_t *>(static_cast<const char *>(d) + seg_bytes + gseg_bytes + span_bytes);
+    p.d_mx_buckets =
+        reinterpret_cast<const MxBucket *>(static_cast<const char *>(d) + seg_bytes + gseg_bytes + span_bytes);
+    p.d_gather_group = reinterpret_cast<const uint32_t *>(static_cast<const char *>(d) + index_at);
+    p.d_mx_tile_group = p.d_gather_group + gather_group.size();
+    p.d_mx_unit_group = p.d_mx_tile_group + mx_tile_group.size();
     p.device = dev;
     if (hipDeviceGetAttribute(&p.lds_per_cu, hipDeviceAttributeMaxSharedMemoryPerMultiprocessor, dev) !=
         hipSuccess) {

@@ -68,6 +68,27 @@ inline int64_t range_tiles(int64_t rb, int64_t len) {
     return (rb + len - tile_origin(rb) + kGatherTile - 1) / kGatherTile;
 }
 
+// One bucket as the MXFP4 storage (zdo_mx.h) and its kernels see it. Every
+// rank's range of the bucket has the same number of storage tiles (kTileElems
+// slots, 16 blocks of 32), whatever its phase modulo kAnchor, so a tile of
+// any rank is found from this one entry. Kernels that take kMxUnit tiles at a
+// time walk units instead; a unit never spans two ranges.
+constexpr int kMxBlock = 32;
+constexpr int kMxTileBlocks = kTileElems / kMxBlock;
+constexpr int kMxUnit = 4;
+struct MxBucket {
+    int64_t offset, numel, shard;  // WORLD start, parameter elements, range length
+    int64_t base;                  // LOCAL start of the rank's range
+    int64_t tile0, unit0;          // first tile and unit of the rank's range in LOCAL storage
+    int32_t tiles, units;          // per range
+};
+inline int64_t mx_range_tiles(int64_t shard_numel) {
+    return (shard_numel + kAnchor - 1 + kTileElems - 1) / kTileElems;
+}
+// Storage of more tiles than this (5.5e11 slots, 290 GB) is refused: tile
+// numbers stay within 32 bits.
+constexpr int64_t kMxMaxTiles = int64_t(1) << 30;
+
 void set_error(const std::string &msg);
 
 }  // namespace zdo
@@ -90,13 +111,20 @@ struct zdo_plan {
     // (bucket-major, rank-minor).
     std::vector<zdo::RangeSpan> gather_ranges;
     int64_t gather_tiles = 0;
+    // The MXFP4 storage: per bucket, and the tiles and units of one rank's
+    // ranges.
+    std::vector<zdo::MxBucket> mx_buckets;
+    int64_t mx_tiles = 0, mx_units = 0;
     // Device copies, in one allocation on `device`: both segment lists, the
-    // gather ranges, and the kTileGroup index of each launch space.
+    // gather ranges, the MXFP4 buckets, and the kTileGroup index of each
+    // launch space.
     void *d_table = nullptr;
     const zdo::Seg *d_param_segs = nullptr, *d_range_segs = nullptr;
     const zdo::GroupSeg *d_param_group = nullptr, *d_range_group = nullptr;
     const zdo::RangeSpan *d_gather_ranges = nullptr;
     const uint32_t *d_gather_group = nullptr;
+    const zdo::MxBucket *d_mx_buckets = nullptr;
+    const uint32_t *d_mx_tile_group = nullptr, *d_mx_unit_group = nullptr;
     int device = -1;
     int lds_per_cu = 0;   // bytes of LDS per compute unit on `device`
 };
