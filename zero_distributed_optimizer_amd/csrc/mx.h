@@ -49,7 +49,6 @@ struct MxStepArgs {
     uint8_t *codes, *scales;  // may be NULL (both)
     float *main_grad;       // may be NULL
     const float *coeff;     // may be NULL
-    int64_t state_numel;
     AdamConst c;
 };
 

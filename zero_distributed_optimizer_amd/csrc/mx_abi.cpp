@@ -316,7 +316,6 @@ int sharded_adam_step_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32_t 
         a.scales = param_scales;
         a.main_grad = main_grad_out;
         a.coeff = grad_coeff;
-        a.state_numel = L;
         a.c = adam_const(*hp);
         return launch_result(launch_mx_step(a, plan->lds_per_cu, static_cast<hipStream_t>(stream)), fn);
     });

@@ -72,6 +72,20 @@ __device__ __forceinline__ MxTile local_tile(const MxWalk &wk, int64_t i) {
     return tile_in(b, wk.dp, wk.rank, int(x - b->tile0));
 }
 
+// The walk index that launch slot i takes. As in the bf16 kernels, a short
+// launch hands each of the 8 XCDs 8 consecutive tiles out of every 64: those
+// 8 tiles' scales are one 128-byte line of every contribution. Measured with
+// and without: step, GPT-2 small rank 80.3 and 82.7 us, 64 contributions of
+// 1e7 elements 107.4 and 109.5 us; long launches are slower with it
+// (Llama-3-8B rank 4993 and 4976 us) and keep the dispatch order.
+constexpr int64_t kShortLaunch = int64_t(1) << 17;
+__device__ __forceinline__ int64_t launch_order(int64_t count, int64_t i) {
+    if (count >= kShortLaunch || i >= count / 64 * 64)
+        return i;
+    const int64_t r = i % 64;
+    return i - r + (r % 8) * 8 + r / 8;
+}
+
 // A unit of up to kMxUnit consecutive tiles of one range: its first tile's
 // number within the range and how many there are.
 struct MxUnit {
@@ -114,6 +128,13 @@ __device__ __forceinline__ void values_of(uint32_t codes, float scale, float x[8
     x[7] = d[1];
 }
 
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// The largest over the 4 lanes of a quad: 1 and 2 lanes away.
+__device__ __forceinline__ uint32_t max_quad(uint32_t x) {
+    x = max_bits(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0xB1, 0xf, 0xf, true)));
+    return max_bits(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x4E, 0xf, 0xf, true)));
+}
+
 // A lane's 8 values to a word of codes, with the scale of its block (4
 // lanes): the largest magnitude's bits over the block, by integer compare, so
 // that Inf and NaN win; byte = max(0, exponent - 2). Every lane of the wave
@@ -121,26 +142,18 @@ __device__ __forceinline__ void values_of(uint32_t codes, float scale, float x[8
 __device__ __forceinline__ void round_block(const float x[8], uint32_t &codes, uint32_t &byte) {
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
-        top = a > top ? a : top;
-    }
-    // lanes 1 and 2 away within the quad
-    const uint32_t t1 = uint32_t(__builtin_amdgcn_mov_dpp(int(top), 0xB1, 0xf, 0xf, true));
-    top = t1 > top ? t1 : top;
-    const uint32_t t2 = uint32_t(__builtin_amdgcn_mov_dpp(int(top), 0x4E, 0xf, 0xf, true));
-    top = t2 > top ? t2 : top;
+    for (int e = 0; e < 8; ++e)
+        top = max_bits(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    top = max_quad(top);
     const uint32_t ex = top >> 23;
-    byte = ex > 2 ? ex - 2 : 0;
+    byte = ex == 255 ? 255 : ex > 2 ? ex - 2 : 0;
     const float s = scale_f32(byte);
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], s, 0);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], s, 2);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], s, 3);
-    const bool bad = ex == 255;
-    codes = bad ? 0 : c;
-    byte = bad ? 255 : byte;
+    codes = ex == 255 ? 0 : c;
 }
 
 // The lane's word of codes of tile t, and its block's scale.
@@ -155,16 +168,40 @@ __device__ __forceinline__ void st_block(uint8_t *codes, uint8_t *scales, int64_
         scales[t * kMxTileBlocks + threadIdx.x / 4] = uint8_t(s);
 }
 
+// The same for a lane's quad h of tile t, whose blocks are 8 lanes: 16 bits of
+// codes a lane.
+__device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t t, int h, const float x[4]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        top = max_bits(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    top = max_quad(top);
+    // the other quad of the 8 lanes: the mirror image within them
+    top = max_bits(top, uint32_t(__builtin_amdgcn_mov_dpp(int(top), 0x141, 0xf, 0xf, true)));
+    const uint32_t ex = top >> 23, byte = ex == 255 ? 255 : ex > 2 ? ex - 2 : 0;
+    const float s = scale_f32(byte);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
+    reinterpret_cast<uint16_t *>(codes + t * (kTileElems / 2))[64 * h + threadIdx.x] = ex == 255 ? 0 : uint16_t(c);
+    if (threadIdx.x % 8 == 0)
+        scales[t * kMxTileBlocks + 8 * h + threadIdx.x / 8] = uint8_t(byte);
+}
+
 // The sum of the contributions over the lane's 8 slots of tile t, in the
-// order given, from -0 (which adds to any first term exactly). Batches of
-// kBatch contributions have their loads in flight together.
-constexpr int kBatch = 8;
+// order given, from -0 (which adds to any first term exactly). kN = 8 or 16:
+// that many contributions, all their loads in flight together; kN = 0: any
+// number, in batches of 16 and what is left, each batch's loads in flight
+// together. (A batch of the same code for any count up to 16, its loads
+// behind uniform branches, took 1.9 times as long at 16 contributions and 4
+// times at 32: the waits behind a branch are for every load.)
+constexpr int kBatch = 16;
 template <int kCount>
-__device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t t, float acc[8]) {
+__device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t at, float acc[8]) {
     uint32_t c[kCount], s[kCount];
 #pragma unroll
     for (int i = 0; i < kCount; ++i)
-        ld_block(in.codes[j + i], in.scales[j + i], t, c[i], s[i]);
+        ld_block(in.codes[j + i], in.scales[j + i], at, c[i], s[i]);
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
         float x[8];
@@ -174,24 +211,33 @@ __device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t t, 
             acc[e] = acc[e] + x[e];
     }
 }
+template <int kN>
 __device__ __forceinline__ void sum_blocks(const MxInputs &in, const MxTile &t, float acc[8]) {
     const int64_t at = in.world ? t.world : t.local;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         acc[e] = -0.0f;
-    int j = 0;
-    for (; j + kBatch <= in.n; j += kBatch)
-        add_batch<kBatch>(in, j, at, acc);
-    if (in.n & 4) {
-        add_batch<4>(in, j, at, acc);
-        j += 4;
+    if constexpr (kN > 0) {
+        add_batch<kN>(in, 0, at, acc);
+    } else {
+        int j = 0;
+        for (; j + kBatch <= in.n; j += kBatch)
+            add_batch<kBatch>(in, j, at, acc);
+        if (in.n & 8) {
+            add_batch<8>(in, j, at, acc);
+            j += 8;
+        }
+        switch (in.n & 7) {
+        case 1: add_batch<1>(in, j, at, acc); break;
+        case 2: add_batch<2>(in, j, at, acc); break;
+        case 3: add_batch<3>(in, j, at, acc); break;
+        case 4: add_batch<4>(in, j, at, acc); break;
+        case 5: add_batch<5>(in, j, at, acc); break;
+        case 6: add_batch<6>(in, j, at, acc); break;
+        case 7: add_batch<7>(in, j, at, acc); break;
+        default: break;
+        }
     }
-    if (in.n & 2) {
-        add_batch<2>(in, j, at, acc);
-        j += 2;
-    }
-    if (in.n & 1)
-        add_batch<1>(in, j, at, acc);
 }
 
 // The lane's slots of its chunk below `end` of tile slots [lo, end).
@@ -221,13 +267,14 @@ __device__ __forceinline__ void st_bf16(uint16_t *p, const float x[8], Slots s) 
 
 // ---- kernels -------------------------------------------------------------------------------------
 
+template <int kN>
 __global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const MxTile t = local_tile(a.walk, i);
+        const MxTile t = local_tile(a.walk, launch_order(a.walk.count, i));
         if (t.lo >= t.hi)
             continue;
         float acc[8];
-        sum_blocks(a.in, t, acc);
+        sum_blocks<kN>(a.in, t, acc);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             acc[e] = acc[e] * a.scale;
@@ -235,13 +282,15 @@ __global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
     }
 }
 
+template <int kN>
 __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const MxTile t = local_tile(a.walk, i);
+        const int64_t x = launch_order(a.walk.count, i);
+        const MxTile t = local_tile(a.walk, x);
         double s = 0.0;
         if (t.lo < t.own) {
             float acc[8];
-            sum_blocks(a.in, t, acc);
+            sum_blocks<kN>(a.in, t, acc);
             const Slots own = slots_of(t.lo, t.own);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -254,83 +303,151 @@ __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
         for (int off = 32; off > 0; off >>= 1)
             s = s + __shfl_xor(s, off, 64);
         if (threadIdx.x == 0)
-            a.partial[i] = s;
+            a.partial[x] = s;
     }
 }
 
-template <bool kNT>
-__global__ __launch_bounds__(kBlock) void mx_step_kernel(MxStepArgs a) {
+// ---- the step --------------------------------------------------------------------------------
+// The state is read and rewritten once and a training step finds it cold:
+// its accesses are non-temporal (GPT-2 small rank, 187 MB of state, three
+// states in turn: 80.3 us, with plain accesses 87.2; back to back on one
+// state 79.1 and 77.7; Llama-3-8B rank 4973 and 5274 us).
+
+// A tile that lies whole inside the rank's elements. The state goes by
+// quads: lane l takes slots [4l, 4l + 4) and [256 + 4l, 256 + 4l + 4), so that
+// every access of the wave covers 1 KiB without a gap (by 8 consecutive
+// slots a lane, every second 16 bytes: 8.43 ms instead of 4.97 on the
+// Llama-3-8B rank). The codes go by chunks of 8 slots (a word a lane; by quads,
+// in half words, 5.02 ms), and the sums change lanes through 2 KiB of LDS.
+template <int kN>
+__device__ __forceinline__ void step_whole(const MxStepArgs &a, const MxTile &t, bool clip, float cf, f32x4 *sums) {
+    const int lane = int(threadIdx.x);
+    f32x4 pv[2], mv[2], vv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t k = t.k + h * (kTileElems / 2) + 4 * lane;
+        pv[h] = ld_state<true>(a.master + k);
+        mv[h] = ld_state<true>(a.m + k);
+        vv[h] = ld_state<true>(a.v + k);
+    }
+    float acc[8];
+    sum_blocks<kN>(a.in, t, acc);
+    sums[2 * lane] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+    sums[2 * lane + 1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+    __syncthreads();
+    f32x4 g[2] = {sums[lane], sums[64 + lane]};
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = h * (kTileElems / 2) + 4 * lane, k = t.k + at;
+        float p[4], m[4], v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            g[h][e] = g[h][e] * a.scale;
+            if (clip)
+                g[h][e] = g[h][e] * cf;
+            p[e] = pv[h][e];
+            m[e] = mv[h][e];
+            v[e] = vv[h][e];
+            adam(a.c, g[h][e], p[e], m[e], v[e]);
+        }
+        st_state<true>(a.master + k, f32x4{p[0], p[1], p[2], p[3]});
+        st_state<true>(a.m + k, f32x4{m[0], m[1], m[2], m[3]});
+        st_state<true>(a.v + k, f32x4{v[0], v[1], v[2], v[3]});
+        if (a.main_grad)
+            stf4_out(a.main_grad + k, g[h]);
+        if (a.param)
+            __builtin_nontemporal_store(u32x2{to_bf16x2(p[0], p[1]), to_bf16x2(p[2], p[3])},
+                                        reinterpret_cast<u32x2 *>(a.param + (a.param_local ? t.k : t.w) + at));
+        if (a.codes)
+            st_quad(a.codes, a.scales, a.mx_world ? t.world : t.local, h, p);
+    }
+}
+
+// Any other tile, by chunks.
+__device__ __forceinline__ void step_edge(const MxStepArgs &a, const MxTile &t, bool clip, float cf) {
+    const Slots own = slots_of(t.lo, t.own);
+    const int64_t k = t.k + threadIdx.x * kChunk;
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        p[e] = 0.0f;
+    if (t.lo < t.own) {
+        float m[8], v[8], g[8];
+        if (own.full()) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 pv = ld_state<true>(a.master + k + 4 * h), mv = ld_state<true>(a.m + k + 4 * h),
+                            vv = ld_state<true>(a.v + k + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[4 * h + e] = pv[e];
+                    m[4 * h + e] = mv[e];
+                    v[4 * h + e] = vv[e];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = e >= own.lo && e < own.hi;
+                p[e] = in ? a.master[k + e] : 0.0f;
+                m[e] = in ? a.m[k + e] : 0.0f;
+                v[e] = in ? a.v[k + e] : 0.0f;
+            }
+        }
+        sum_blocks<0>(a.in, t, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] = g[e] * a.scale;
+            if (clip)
+                g[e] = g[e] * cf;
+            if (e >= own.lo && e < own.hi)
+                adam(a.c, g[e], p[e], m[e], v[e]);
+        }
+        if (own.full()) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                st_state<true>(a.master + k + 4 * h, f32x4{p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]});
+                st_state<true>(a.m + k + 4 * h, f32x4{m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]});
+                st_state<true>(a.v + k + 4 * h, f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+                if (a.main_grad)
+                    stf4_out(a.main_grad + k + 4 * h, f32x4{g[4 * h], g[4 * h + 1], g[4 * h + 2], g[4 * h + 3]});
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= own.lo && e < own.hi) {
+                    a.master[k + e] = p[e];
+                    a.m[k + e] = m[e];
+                    a.v[k + e] = v[e];
+                    if (a.main_grad)
+                        a.main_grad[k + e] = g[e];
+                }
+        }
+        if (a.param)
+            st_bf16(a.param + (a.param_local ? k : t.w + threadIdx.x * kChunk), p, own);
+    }
+    if (a.codes) {
+        uint32_t c, s;
+        round_block(p, c, s);
+        st_block(a.codes, a.scales, a.mx_world ? t.world : t.local, c, s);
+    }
+}
+
+// The occupancy bounds let the compiler keep every load of a batch in
+// flight; the launches cap the waves anyway.
+template <int kN>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4))) void mx_step_kernel(MxStepArgs a) {
+    __shared__ f32x4 sums[kTileElems / 4];
     const bool clip = a.coeff != nullptr;
     const float cf = clip ? *ro(a.coeff) : 1.0f;
     const int64_t iend = clip && cf != cf ? 0 : a.walk.count;   // NaN: found-inf, nothing changes
     for (int64_t i = blockIdx.x; i < iend; i += gridDim.x) {
-        const MxTile t = local_tile(a.walk, i);
-        const Slots own = slots_of(t.lo, t.own);
-        const int64_t k = t.k + threadIdx.x * kChunk;
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            p[e] = 0.0f;
-        if (t.lo < t.own) {
-            float m[8], v[8], g[8];
-            if (own.full()) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f32x4 pv = ld_state<kNT>(a.master + k + 4 * h), mv = ld_state<kNT>(a.m + k + 4 * h),
-                                vv = ld_state<kNT>(a.v + k + 4 * h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[4 * h + e] = pv[e];
-                        m[4 * h + e] = mv[e];
-                        v[4 * h + e] = vv[e];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool in = e >= own.lo && e < own.hi;
-                    p[e] = in ? a.master[k + e] : 0.0f;
-                    m[e] = in ? a.m[k + e] : 0.0f;
-                    v[e] = in ? a.v[k + e] : 0.0f;
-                }
-            }
-            sum_blocks(a.in, t, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                g[e] = g[e] * a.scale;
-                if (clip)
-                    g[e] = g[e] * cf;
-                if (e >= own.lo && e < own.hi)
-                    adam(a.c, g[e], p[e], m[e], v[e]);
-            }
-            if (own.full()) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    st_state<kNT>(a.master + k + 4 * h, f32x4{p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]});
-                    st_state<kNT>(a.m + k + 4 * h, f32x4{m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]});
-                    st_state<kNT>(a.v + k + 4 * h, f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
-                    if (a.main_grad)
-                        stf4_out(a.main_grad + k + 4 * h, f32x4{g[4 * h], g[4 * h + 1], g[4 * h + 2], g[4 * h + 3]});
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e >= own.lo && e < own.hi) {
-                        a.master[k + e] = p[e];
-                        a.m[k + e] = m[e];
-                        a.v[k + e] = v[e];
-                        if (a.main_grad)
-                            a.main_grad[k + e] = g[e];
-                    }
-            }
-            if (a.param)
-                st_bf16(a.param + (a.param_local ? k : t.w + threadIdx.x * kChunk), p, own);
-        }
-        if (a.codes) {
-            uint32_t c, s;
-            round_block(p, c, s);
-            st_block(a.codes, a.scales, a.mx_world ? t.world : t.local, c, s);
-        }
+        const MxTile t = local_tile(a.walk, launch_order(a.walk.count, i));
+        if (t.lo == 0 && t.own == kTileElems)
+            step_whole<kN>(a, t, clip, cf, sums);
+        else
+            step_edge(a, t, clip, cf);
     }
 }
 
@@ -433,16 +550,36 @@ __global__ __launch_bounds__(kBlock) void mx_gather_kernel(MxGatherArgs a) {
 
 }  // namespace
 
+#ifndef MX_REDUCE_WAVES
+#define MX_REDUCE_WAVES 0
+#endif
+#ifndef MX_REDUCE_WAVES_SHORT
+#define MX_REDUCE_WAVES_SHORT 0
+#endif
 hipError_t launch_mx_reduce(const MxReduceArgs &a, int lds_per_cu, hipStream_t stream) {
     if (a.walk.count <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(mx_reduce_kernel, dim3(grid_for(a.walk.count)), dim3(kBlock), 0, stream, a);
+    const dim3 grid(grid_for(a.walk.count)), block(kBlock);
+    const unsigned lds =
+        lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? MX_REDUCE_WAVES_SHORT : MX_REDUCE_WAVES);
+    switch (a.in.n) {
+    case 8: hipLaunchKernelGGL(mx_reduce_kernel<8>, grid, block, lds, stream, a); break;
+    case 16: hipLaunchKernelGGL(mx_reduce_kernel<16>, grid, block, lds, stream, a); break;
+    default: hipLaunchKernelGGL(mx_reduce_kernel<0>, grid, block, lds, stream, a); break;
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream) {
     if (a.walk.count > 0) {
-        hipLaunchKernelGGL(mx_norm_kernel, dim3(grid_for(a.walk.count)), dim3(kBlock), 0, stream, a);
+        const dim3 grid(grid_for(a.walk.count)), block(kBlock);
+        const unsigned lds =
+            lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? MX_REDUCE_WAVES_SHORT : MX_REDUCE_WAVES);
+        switch (a.in.n) {
+        case 8: hipLaunchKernelGGL(mx_norm_kernel<8>, grid, block, lds, stream, a); break;
+        case 16: hipLaunchKernelGGL(mx_norm_kernel<16>, grid, block, lds, stream, a); break;
+        default: hipLaunchKernelGGL(mx_norm_kernel<0>, grid, block, lds, stream, a); break;
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -450,14 +587,30 @@ hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, int lds_per_cu, 
     return launch_tile_sums(a.partial, a.walk.count, norm_sq, stream);
 }
 
+// Waves that share a compute unit in the step. Long launches, Llama-3-8B
+// shapes: 8 contributions with all loads in flight 4958 us at 9 waves (8:
+// 4961, 10: 4982, 12: 5075, 6: 5926; in batches 5041 at 12), 16 2898 us (10:
+// 3014; in batches 3027); other counts 14 (3 contributions: 1331, at 12 1342
+// and at 16 1381; 32: 1854, 1850 and 1847; 12: 845, 860 and 840). Short
+// launches take 16 (GPT-2 small rank: the same from 10 up; fragmented, 16
+// contributions: 34.6 us, 36.3 at 10).
+constexpr int kStepWavesFixed = 9, kStepWaves = 14, kStepWavesShort = 16;
+
 hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t stream) {
     if (a.walk.count <= 0)
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
-    if (state_nontemporal(a.state_numel))
-        hipLaunchKernelGGL(mx_step_kernel<true>, grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL(mx_step_kernel<false>, grid, block, 0, stream, a);
+    const bool fixed = a.in.n == 8 || a.in.n == 16;
+    const unsigned cap = lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? kStepWavesShort
+                                                   : fixed                     ? kStepWavesFixed
+                                                                               : kStepWaves);
+    constexpr unsigned own = kTileElems * sizeof(float);   // the kernel's LDS
+    const unsigned lds = cap > own ? cap - own : 0;
+    switch (a.in.n) {
+    case 8: hipLaunchKernelGGL(mx_step_kernel<8>, grid, block, lds, stream, a); break;
+    case 16: hipLaunchKernelGGL(mx_step_kernel<16>, grid, block, lds, stream, a); break;
+    default: hipLaunchKernelGGL(mx_step_kernel<0>, grid, block, lds, stream, a); break;
+    }
     return hipGetLastError();
 }
 
