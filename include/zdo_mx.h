@@ -96,8 +96,9 @@ int reduce_scatter_local_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32
 /* The squared norm of the gradient that sharded_adam_step_mxfp4 steps with:
  * sum of g^2 over the rank's owned parameter elements, g = scale * (x_0 + x_1
  * + ...) in fp32 as above, squares (exact) and sums in fp64, in an order that
- * depends on the plan only: per tile (a lane's 8 slots in order, then a fixed
- * butterfly over 64 lanes) into `workspace`, then grad_norm_sq's two levels.
+ * depends on the plan and n only: per run of 1 or up to 4 tiles (a lane's
+ * slots in order, then a fixed butterfly over 64 lanes) into `workspace`,
+ * then grad_norm_sq's two levels.
  * workspace: zdo_plan_norm_mxfp4_workspace_bytes(plan) bytes, 16-byte
  * aligned, this call's alone until it completes. norm_sq_out: device double.
  * A rank that owns nothing gets 0. A block with scale 255 makes it NaN, and

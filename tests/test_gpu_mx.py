@@ -15,6 +15,8 @@ import oracle.mx as MX
 import oracle.numerics as ON
 import oracle.step as OS
 import workloads as W
+import zero_distributed_optimizer_amd as Z
+from zero_distributed_optimizer_amd import build as ZB
 from test_gpu_clip import assert_norm
 from test_gpu_parity import (DEV, SENTINEL, assert_bf16, assert_f32, bf16_host, free, host_f32, host_u16, hp_kwargs,
                              to_dev)
@@ -55,6 +57,18 @@ def random_mx(rng, lay, coords, lo=110, hi=130):
 def state_of(rng, n):
     return [(rng.standard_normal(n) * 0.02).astype(np.float32), (rng.standard_normal(n) * 1e-3).astype(np.float32),
             ((rng.standard_normal(n) * 1e-3) ** 2 + 1e-12).astype(np.float32)]
+
+
+@pytest.fixture(params=["library", "long forms"])
+def either(gpu, request):
+    """The library, and the build that takes the forms for long launches at
+    any length, with 64 workgroups at most."""
+    if request.param == "library":
+        yield gpu
+        return
+    with Z.use_library(ZB.GRID_LOOP_LIB):
+        yield gpu
+        free()
 
 
 # ---- quantising ------------------------------------------------------------------------------
@@ -153,7 +167,8 @@ def sources(gpu, rng, lay, r, D, coords, **kw):
 
 
 @pytest.mark.parametrize("seed", range(14))
-def test_reduce_random_layouts(gpu, seed):
+def test_reduce_random_layouts(either, seed):
+    gpu = either
     pr, sizes, bucket, D = layout_of(300 + seed)
     rng = np.random.default_rng(seed)
     lay = OL.build_layout(sizes, bucket, D)
@@ -177,9 +192,10 @@ def test_reduce_random_layouts(gpu, seed):
 
 
 @pytest.mark.parametrize("n", range(1, 20))
-def test_reduce_every_small_count(gpu, n):
+def test_reduce_every_small_count(either, n):
     """Every number of contributions around the kernels' batches, at scales
     far enough apart that the order of the sum shows."""
+    gpu = either
     rng = np.random.default_rng(n)
     lay = OL.build_layout([2500], 2500, 1)
     plan = gpu.build_range_map([2500], 2500, 1, 0)
@@ -190,9 +206,10 @@ def test_reduce_every_small_count(gpu, n):
     assert_bf16(host_u16(out), want, f"n={n}")
 
 
-def test_values_of_every_code_and_scale(gpu):
+def test_values_of_every_code_and_scale(either):
     """One contribution, scale 1: all 256 scales x 16 codes, in bf16; scale 255
     is NaN, 2^127 times 2 and more overflows, 2^-127 times 0.5 is subnormal."""
+    gpu = either
     n = 256 * 32
     lay = OL.build_layout([n], n, 1)
     plan = gpu.build_range_map([n], n, 1, 0)
@@ -210,8 +227,43 @@ def test_values_of_every_code_and_scale(gpu):
     assert_bf16(host_u16(out), want, "gather")
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 8, 13, 16, 32, 45])
+def test_long_reductions(gpu, n):
+    """20 M slots in ragged buckets: the forms for long launches, reduction and
+    norm, at a fresh order of three storages."""
+    sizes, bucket, D = [7_000_001, 65, 4_999_999, 33, 8_000_011], 6_000_000, 1
+    lay = OL.build_layout(sizes, bucket, D)
+    plan = gpu.build_range_map(sizes, bucket, D, 0)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    blocks, L = plan.mx_blocks(gpu.LOCAL), plan.shard_numel
+    three = [(torch.randint(0, 256, (blocks, 16), dtype=torch.uint8, device=DEV, generator=gen),
+              torch.randint(112, 128, (blocks,), dtype=torch.uint8, device=DEV, generator=gen)) for _ in range(3)]
+    order = [(j * j + j // 3) % 3 for j in range(n)]
+    out = torch.full((L,), SENTINEL, dtype=torch.int16, device=DEV)
+    gpu.reduce_scatter_local_mxfp4(plan, [three[j] for j in order], gpu.LOCAL, 0.3, out, gpu.LOCAL)
+    ws = torch.empty(plan.norm_mxfp4_workspace_bytes, dtype=torch.uint8, device=DEV)
+    ns = torch.zeros(1, dtype=torch.float64, device=DEV)
+    gpu.grad_norm_sq_mxfp4(plan, [three[j] for j in order], gpu.LOCAL, 0.3, ws, ns)
+    host, got, total = [host_mx(s) for s in three], host_u16(out), 0.0
+    for b, rng in enumerate(MX.ranges(lay, 0)):
+        v = [MX._values(s, MX.LOCAL, rng).astype(np.float32) for s in host]
+        acc = v[order[0]]
+        for j in order[1:]:
+            acc = acc + v[j]
+        acc = acc * np.float32(0.3)
+        s = slice(rng[2], rng[2] + acc.size)
+        assert_bf16(got[s], ON.narrow(acc), f"bucket {b}")
+        got[s] = SENTINEL
+        own = acc[:rng[1] - rng[0].start].astype(np.float64)
+        total += float(np.sum(own * own))
+    assert (got == SENTINEL).all()
+    assert_norm(float(ns), total, plan.owned_numel, "norm")
+    free()
+
+
 @pytest.mark.parametrize("seed", range(6))
-def test_norm(gpu, seed):
+def test_norm(either, seed):
+    gpu = either
     pr, sizes, bucket, D = layout_of(500 + seed)
     rng = np.random.default_rng(seed)
     lay = OL.build_layout(sizes, bucket, D)
@@ -620,8 +672,6 @@ def test_calls_on_another_stream(gpu):
 def test_loops_beyond_the_grid(gpu):
     """Every MXFP4 kernel through the build whose launches are capped at 64
     workgroups: the whole loop, against the library's."""
-    import zero_distributed_optimizer_amd as Z
-    from zero_distributed_optimizer_amd import build as ZB
     sizes, bucket, D = [300000, 17, 123456, 2049], 200000, 4
     loop = Loop(gpu, sizes, bucket, D)
     ref = loop.device()

@@ -25,7 +25,7 @@ struct MxInputs {
 };
 
 struct MxReduceArgs {
-    MxWalk walk;  // LOCAL tiles
+    MxWalk walk, units;  // the same buckets' LOCAL tiles and units
     MxInputs in;
     int32_t out_local;
     float scale;
@@ -33,10 +33,10 @@ struct MxReduceArgs {
 };
 
 struct MxNormArgs {
-    MxWalk walk;  // LOCAL tiles
+    MxWalk walk, units;  // LOCAL tiles, and units
     MxInputs in;
     float scale;
-    double *partial;  // one per tile
+    double *partial;  // one per tile or unit
 };
 
 struct MxStepArgs {

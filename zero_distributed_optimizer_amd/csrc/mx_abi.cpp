@@ -215,6 +215,7 @@ int reduce_scatter_local_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32
         if (int rc = bufs.check(fn))
             return rc;
         a.walk = walk_of(plan, bucket_begin, bucket_end, false, false);
+        a.units = walk_of(plan, bucket_begin, bucket_end, true, false);
         a.out_local = out_coords == ZDO_LOCAL;
         a.scale = scale;
         a.out = out;
@@ -243,6 +244,7 @@ int grad_norm_sq_mxfp4(const zdo_plan *plan, const uint8_t *const *codes, const 
         if (int rc = bufs.check(fn))
             return rc;
         a.walk = walk_of(plan, 0, nbuckets(plan), false, false);
+        a.units = walk_of(plan, 0, nbuckets(plan), true, false);
         a.scale = scale;
         a.partial = static_cast<double *>(workspace);
         return launch_result(launch_mx_norm(a, norm_sq_out, plan->lds_per_cu, static_cast<hipStream_t>(stream)), fn);

@@ -188,57 +188,67 @@ __device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t
         scales[t * kMxTileBlocks + 8 * h + threadIdx.x / 8] = uint8_t(byte);
 }
 
-// The sum of the contributions over the lane's 8 slots of tile t, in the
-// order given, from -0 (which adds to any first term exactly). kN = 8 or 16:
-// that many contributions, all their loads in flight together; kN = 0: any
-// number, in batches of 16 and what is left, each batch's loads in flight
-// together. (A batch of the same code for any count up to 16, its loads
-// behind uniform branches, took 1.9 times as long at 16 contributions and 4
-// times at 32: the waits behind a branch are for every load.)
+// The sum of the contributions over the lane's 8 * kW slots of kW consecutive
+// tiles from tile `at` (lane l: slots [8 kW l, 8 kW (l + 1)), which lie in one
+// block), in the order given, from -0 (which adds to any first term
+// exactly). kN > 0: that many contributions, all their loads in flight
+// together; kN = 0: any number, in batches of 16 and what is left, each
+// batch's loads in flight together. (A batch of the same code for any count up
+// to 16, its loads behind uniform branches, took 1.9 times as long at 16
+// contributions and 4 times at 32: the waits behind a branch are for every
+// load.)
 constexpr int kBatch = 16;
-template <int kCount>
-__device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t at, float acc[8]) {
-    uint32_t c[kCount], s[kCount];
-#pragma unroll
-    for (int i = 0; i < kCount; ++i)
-        ld_block(in.codes[j + i], in.scales[j + i], at, c[i], s[i]);
+template <int kW, int kCount>
+__device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t at, float acc[8 * kW]) {
+    typedef unsigned int words __attribute__((ext_vector_type(kW)));
+    words c[kCount];
+    uint32_t s[kCount];
+    const int lane = int(threadIdx.x);
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-        float x[8];
-        values_of(c[i], scale_f32(s[i]), x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            acc[e] = acc[e] + x[e];
+        c[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const words *>(in.codes[j + i] + at * (kTileElems / 2)) + lane);
+        s[i] = in.scales[j + i][at * kMxTileBlocks + lane * kW / 4];
     }
-}
-template <int kN>
-__device__ __forceinline__ void sum_blocks(const MxInputs &in, const MxTile &t, float acc[8]) {
-    const int64_t at = in.world ? t.world : t.local;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int i = 0; i < kCount; ++i)
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            float x[8];
+            values_of(c[i][w], scale_f32(s[i]), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                acc[8 * w + e] = acc[8 * w + e] + x[e];
+        }
+}
+template <int kW, int kN>
+__device__ __forceinline__ void sum_blocks(const MxInputs &in, int64_t at, float acc[8 * kW]) {
+#pragma unroll
+    for (int e = 0; e < 8 * kW; ++e)
         acc[e] = -0.0f;
     if constexpr (kN > 0) {
-        add_batch<kN>(in, 0, at, acc);
+        add_batch<kW, kN>(in, 0, at, acc);
     } else {
         int j = 0;
         for (; j + kBatch <= in.n; j += kBatch)
-            add_batch<kBatch>(in, j, at, acc);
+            add_batch<kW, kBatch>(in, j, at, acc);
         if (in.n & 8) {
-            add_batch<8>(in, j, at, acc);
+            add_batch<kW, 8>(in, j, at, acc);
             j += 8;
         }
         switch (in.n & 7) {
-        case 1: add_batch<1>(in, j, at, acc); break;
-        case 2: add_batch<2>(in, j, at, acc); break;
-        case 3: add_batch<3>(in, j, at, acc); break;
-        case 4: add_batch<4>(in, j, at, acc); break;
-        case 5: add_batch<5>(in, j, at, acc); break;
-        case 6: add_batch<6>(in, j, at, acc); break;
-        case 7: add_batch<7>(in, j, at, acc); break;
+        case 1: add_batch<kW, 1>(in, j, at, acc); break;
+        case 2: add_batch<kW, 2>(in, j, at, acc); break;
+        case 3: add_batch<kW, 3>(in, j, at, acc); break;
+        case 4: add_batch<kW, 4>(in, j, at, acc); break;
+        case 5: add_batch<kW, 5>(in, j, at, acc); break;
+        case 6: add_batch<kW, 6>(in, j, at, acc); break;
+        case 7: add_batch<kW, 7>(in, j, at, acc); break;
         default: break;
         }
     }
 }
+__device__ __forceinline__ int64_t stored_at(const MxInputs &in, const MxTile &t) { return in.world ? t.world : t.local; }
 
 // The lane's slots of its chunk below `end` of tile slots [lo, end).
 struct Slots {
@@ -267,43 +277,118 @@ __device__ __forceinline__ void st_bf16(uint16_t *p, const float x[8], Slots s) 
 
 // ---- kernels -------------------------------------------------------------------------------------
 
-template <int kN>
-__global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
-    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const MxTile t = local_tile(a.walk, launch_order(a.walk.count, i));
-        if (t.lo >= t.hi)
-            continue;
-        float acc[8];
-        sum_blocks<kN>(a.in, t, acc);
+// One tile of the reduction, whole or not.
+__device__ __forceinline__ void reduce_tile(const MxReduceArgs &a, const MxTile &t) {
+    if (t.lo >= t.hi)
+        return;
+    float acc[8];
+    sum_blocks<1, 0>(a.in, stored_at(a.in, t), acc);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            acc[e] = acc[e] * a.scale;
-        st_bf16(a.out + (a.out_local ? t.k : t.w) + threadIdx.x * kChunk, acc, slots_of(t.lo, t.hi));
+    for (int e = 0; e < 8; ++e)
+        acc[e] = acc[e] * a.scale;
+    st_bf16(a.out + (a.out_local ? t.k : t.w) + threadIdx.x * kChunk, acc, slots_of(t.lo, t.hi));
+}
+
+// Short launches: a tile a wave, for the most waves.
+__global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
+    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x)
+        reduce_tile(a, local_tile(a.walk, launch_order(a.walk.count, i)));
+}
+
+// Long ones: a unit a wave, kW tiles at a time, so that a load instruction
+// covers kW * 256 bytes of codes and kW * 16 scales; the rounded sums change
+// lanes through LDS (16 bytes a chunk, xor-placed against bank conflicts), so
+// that a store covers 1 KiB without a gap.
+__device__ __forceinline__ int chunk_place(int c) { return (c & ~7) | ((c ^ (c >> 3)) & 7); }
+
+template <int kW>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4)))
+void mx_reduce_wide_kernel(MxReduceArgs a) {
+    __shared__ u32x4 chunks[kBlock * kW];
+    const int lane = int(threadIdx.x);
+    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
+        const MxUnit u = unit_at<false>(a.walk, i);
+        int j = 0;
+        for (; j + kW <= u.ntiles; j += kW) {
+            const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
+            if (t.lo != 0 || tile_in(u.b, a.walk.dp, u.rank, u.tile + j + kW - 1).hi != kTileElems)
+                break;
+            float acc[8 * kW];
+            sum_blocks<kW, 0>(a.in, stored_at(a.in, t), acc);
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                u32x4 o;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = to_bf16x2(acc[8 * w + 2 * k] * a.scale, acc[8 * w + 2 * k + 1] * a.scale);
+                chunks[chunk_place(kW * lane + w)] = o;
+            }
+            __syncthreads();
+            uint16_t *out = a.out + (a.out_local ? t.k : t.w);
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const int c = kBlock * w + lane;
+                st16_out(out + c * kChunk, chunks[chunk_place(c)]);
+            }
+            __syncthreads();
+        }
+        for (; j < u.ntiles; ++j)   // the ends of a range
+            reduce_tile(a, tile_in(u.b, a.walk.dp, u.rank, u.tile + j));
     }
 }
 
-template <int kN>
+// The squares of a lane's n slots, those of [lo, hi) only, added in order.
+template <int kSlots>
+__device__ __forceinline__ double add_squares(double s, const float acc[kSlots], float scale, int lo, int hi) {
+#pragma unroll
+    for (int e = 0; e < kSlots; ++e) {
+        const double g = double(acc[e] * scale);
+        if (e >= lo && e < hi)
+            s = s + g * g;
+    }
+    return s;
+}
+__device__ __forceinline__ double norm_tile(const MxNormArgs &a, const MxTile &t, double s) {
+    if (t.lo >= t.own)
+        return s;
+    float acc[8];
+    sum_blocks<1, 0>(a.in, stored_at(a.in, t), acc);
+    const Slots own = slots_of(t.lo, t.own);
+    return add_squares<8>(s, acc, a.scale, own.lo, own.hi);
+}
+__device__ __forceinline__ void put_partial(double *at, double s) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        s = s + __shfl_xor(s, off, 64);
+    if (threadIdx.x == 0)
+        *at = s;
+}
+
+// As the reductions: one partial a tile, or a unit.
 __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
         const int64_t x = launch_order(a.walk.count, i);
-        const MxTile t = local_tile(a.walk, x);
+        put_partial(a.partial + x, norm_tile(a, local_tile(a.walk, x), 0.0));
+    }
+}
+template <int kW>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4)))
+void mx_norm_wide_kernel(MxNormArgs a) {
+    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
+        const MxUnit u = unit_at<false>(a.walk, i);
         double s = 0.0;
-        if (t.lo < t.own) {
-            float acc[8];
-            sum_blocks<kN>(a.in, t, acc);
-            const Slots own = slots_of(t.lo, t.own);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double g = double(acc[e] * a.scale);
-                if (e >= own.lo && e < own.hi)
-                    s = s + g * g;
-            }
+        int j = 0;
+        for (; j + kW <= u.ntiles; j += kW) {
+            const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
+            if (t.lo != 0 || tile_in(u.b, a.walk.dp, u.rank, u.tile + j + kW - 1).own != kTileElems)
+                break;
+            float acc[8 * kW];
+            sum_blocks<kW, 0>(a.in, stored_at(a.in, t), acc);
+            s = add_squares<8 * kW>(s, acc, a.scale, 0, 8 * kW);
         }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1)
-            s = s + __shfl_xor(s, off, 64);
-        if (threadIdx.x == 0)
-            a.partial[x] = s;
+        for (; j < u.ntiles; ++j)
+            s = norm_tile(a, tile_in(u.b, a.walk.dp, u.rank, u.tile + j), s);
+        put_partial(a.partial + i, s);
     }
 }
 
@@ -331,7 +416,7 @@ __device__ __forceinline__ void step_whole(const MxStepArgs &a, const MxTile &t,
         vv[h] = ld_state<true>(a.v + k);
     }
     float acc[8];
-    sum_blocks<kN>(a.in, t, acc);
+    sum_blocks<1, kN>(a.in, stored_at(a.in, t), acc);
     sums[2 * lane] = f32x4{acc[0], acc[1], acc[2], acc[3]};
     sums[2 * lane + 1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
     __syncthreads();
@@ -395,7 +480,7 @@ __device__ __forceinline__ void step_edge(const MxStepArgs &a, const MxTile &t, 
                 v[e] = in ? a.v[k + e] : 0.0f;
             }
         }
-        sum_blocks<0>(a.in, t, g);
+        sum_blocks<1, 0>(a.in, stored_at(a.in, t), g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             g[e] = g[e] * a.scale;
@@ -548,37 +633,67 @@ __global__ __launch_bounds__(kBlock) void mx_gather_kernel(MxGatherArgs a) {
     }
 }
 
+// The form of a reduction of n contributions over `tiles` tiles. Measured,
+// us, a tile a wave / 2 / 4 tiles at a time (waves per compute unit in
+// brackets; 0: no cap):
+//   2.5e8 to 1e9 slots: 8 contributions 1178 / 970 [0] / 985 [0];
+//     16: 917 / 831 [10], 866 [0] / 836 [6]; 32: 885 / 797 [0] / 772 [6],
+//     833 [0]; 64: 854 / 801 [0] / 756 [6]; 3e8 slots: 1: 240 / 158 [0] /
+//     144 [0]; 3: 291 / 203 [0] / 189 [0]; 4: 293 / 191 [0] / 203 [0].
+//   30 M slots: 8: 35.9 / 32.6 / 33.1; 32: 96.3 / 98.7 / 95.9.
+//   15.5 M slots, 8: 19.5 / 20.1 / 20.3; 1e7 slots, 64: 60.2 / 68.4 / 66.2.
+#ifndef ZDO_MX_WIDE_TILES
+#define ZDO_MX_WIDE_TILES (int64_t(1) << 15)
+#endif
+struct ReduceForm {
+    int tiles, waves;
+};
+ReduceForm reduce_form(int n, int64_t tiles) {
+    if (tiles < ZDO_MX_WIDE_TILES)
+        return {1, 0};
+    if (n >= 32)
+        return {4, 6};
+    if (n <= 3)
+        return {4, 0};
+    return {2, n >= 16 ? 10 : 0};
+}
+// LDS to reserve beside the kernel's own.
+unsigned reserve(int lds_per_cu, int waves, unsigned own) {
+    const unsigned cap = lds_for_waves(lds_per_cu, waves);
+    return cap > own ? cap - own : 0;
+}
+
 }  // namespace
 
-#ifndef MX_REDUCE_WAVES
-#define MX_REDUCE_WAVES 0
-#endif
-#ifndef MX_REDUCE_WAVES_SHORT
-#define MX_REDUCE_WAVES_SHORT 0
-#endif
-hipError_t launch_mx_reduce(const MxReduceArgs &a, int lds_per_cu, hipStream_t stream) {
+hipError_t launch_mx_reduce(const MxReduceArgs &args, int lds_per_cu, hipStream_t stream) {
+    MxReduceArgs a = args;
+    const ReduceForm f = reduce_form(a.in.n, a.walk.count);
+    if (f.tiles > 1)
+        a.walk = args.units;
     if (a.walk.count <= 0)
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
-    const unsigned lds =
-        lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? MX_REDUCE_WAVES_SHORT : MX_REDUCE_WAVES);
-    switch (a.in.n) {
-    case 8: hipLaunchKernelGGL(mx_reduce_kernel<8>, grid, block, lds, stream, a); break;
-    case 16: hipLaunchKernelGGL(mx_reduce_kernel<16>, grid, block, lds, stream, a); break;
-    default: hipLaunchKernelGGL(mx_reduce_kernel<0>, grid, block, lds, stream, a); break;
+    const unsigned lds = reserve(lds_per_cu, f.waves, unsigned(f.tiles * kTileElems * sizeof(uint16_t)));
+    switch (f.tiles) {
+    case 2: hipLaunchKernelGGL(mx_reduce_wide_kernel<2>, grid, block, lds, stream, a); break;
+    case 4: hipLaunchKernelGGL(mx_reduce_wide_kernel<4>, grid, block, lds, stream, a); break;
+    default: hipLaunchKernelGGL(mx_reduce_kernel, grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
 }
 
-hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream) {
+hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, int lds_per_cu, hipStream_t stream) {
+    MxNormArgs a = args;
+    const ReduceForm f = reduce_form(a.in.n, a.walk.count);
+    if (f.tiles > 1)
+        a.walk = args.units;
     if (a.walk.count > 0) {
         const dim3 grid(grid_for(a.walk.count)), block(kBlock);
-        const unsigned lds =
-            lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? MX_REDUCE_WAVES_SHORT : MX_REDUCE_WAVES);
-        switch (a.in.n) {
-        case 8: hipLaunchKernelGGL(mx_norm_kernel<8>, grid, block, lds, stream, a); break;
-        case 16: hipLaunchKernelGGL(mx_norm_kernel<16>, grid, block, lds, stream, a); break;
-        default: hipLaunchKernelGGL(mx_norm_kernel<0>, grid, block, lds, stream, a); break;
+        const unsigned lds = reserve(lds_per_cu, f.waves, 0);
+        switch (f.tiles) {
+        case 2: hipLaunchKernelGGL(mx_norm_wide_kernel<2>, grid, block, lds, stream, a); break;
+        case 4: hipLaunchKernelGGL(mx_norm_wide_kernel<4>, grid, block, lds, stream, a); break;
+        default: hipLaunchKernelGGL(mx_norm_kernel, grid, block, 0, stream, a); break;
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
@@ -601,11 +716,11 @@ hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t strea
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
     const bool fixed = a.in.n == 8 || a.in.n == 16;
-    const unsigned cap = lds_for_waves(lds_per_cu, a.walk.count < kShortLaunch ? kStepWavesShort
-                                                   : fixed                     ? kStepWavesFixed
-                                                                               : kStepWaves);
-    constexpr unsigned own = kTileElems * sizeof(float);   // the kernel's LDS
-    const unsigned lds = cap > own ? cap - own : 0;
+    const unsigned lds = reserve(lds_per_cu,
+                                 a.walk.count < kShortLaunch ? kStepWavesShort
+                                 : fixed                     ? kStepWavesFixed
+                                                             : kStepWaves,
+                                 kTileElems * sizeof(float));
     switch (a.in.n) {
     case 8: hipLaunchKernelGGL(mx_step_kernel<8>, grid, block, lds, stream, a); break;
     case 16: hipLaunchKernelGGL(mx_step_kernel<16>, grid, block, lds, stream, a); break;
