@@ -34,7 +34,7 @@ static hipError_t seen(const MxWalk &w) { ++launches; last = w; return hipSucces
 hipError_t launch_mx_reduce(const MxReduceArgs &a, int, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_norm(const MxNormArgs &a, double *, int, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_step(const MxStepArgs &a, int, hipStream_t) { return seen(a.walk); }
-hipError_t launch_mx_quant(const MxQuantArgs &a, int, hipStream_t) { return seen(a.walk); }
+hipError_t launch_mx_quant(const MxQuantArgs &a, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_gather(const MxGatherArgs &a, int, hipStream_t) { return seen(a.walk); }
 }  // namespace zdo
 

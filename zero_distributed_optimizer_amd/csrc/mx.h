@@ -61,7 +61,6 @@ struct MxQuantArgs {
     const float *master;
     float *residual;  // with grads; may be NULL
     uint8_t *codes, *scales;
-    int64_t state_numel;
 };
 
 struct MxGatherArgs {
@@ -73,7 +72,7 @@ struct MxGatherArgs {
 hipError_t launch_mx_reduce(const MxReduceArgs &a, int lds_per_cu, hipStream_t stream);
 hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream);
 hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t stream);
-hipError_t launch_mx_quant(const MxQuantArgs &a, int lds_per_cu, hipStream_t stream);
+hipError_t launch_mx_quant(const MxQuantArgs &a, hipStream_t stream);
 hipError_t launch_mx_gather(const MxGatherArgs &a, int lds_per_cu, hipStream_t stream);
 
 }  // namespace zdo

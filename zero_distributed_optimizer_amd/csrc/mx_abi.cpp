@@ -190,7 +190,7 @@ int quantize_grads_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32_t buc
         a.residual = residual;
         a.codes = codes;
         a.scales = scales;
-        return launch_result(launch_mx_quant(a, plan->lds_per_cu, static_cast<hipStream_t>(stream)), fn);
+        return launch_result(launch_mx_quant(a, static_cast<hipStream_t>(stream)), fn);
     });
 }
 
@@ -346,8 +346,7 @@ int writeback_params_mxfp4(const zdo_plan *plan, const float *master, uint8_t *c
         a.master = master;
         a.codes = codes;
         a.scales = scales;
-        a.state_numel = plan->shard_numel;
-        return launch_result(launch_mx_quant(a, plan->lds_per_cu, static_cast<hipStream_t>(stream)), fn);
+        return launch_result(launch_mx_quant(a, static_cast<hipStream_t>(stream)), fn);
     });
 }
 

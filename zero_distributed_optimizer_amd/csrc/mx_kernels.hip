@@ -162,15 +162,16 @@ __device__ __forceinline__ void ld_block(const uint8_t *codes, const uint8_t *sc
     c = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(codes + t * (kTileElems / 2)) + threadIdx.x);
     s = scales[t * kMxTileBlocks + threadIdx.x / 4];
 }
+// The codes go out non-temporally (quantising 1e9 bf16 elements: 406 us, 482
+// with plain stores; 1.2e8: 54 us both).
 __device__ __forceinline__ void st_block(uint8_t *codes, uint8_t *scales, int64_t t, uint32_t c, uint32_t s) {
-    reinterpret_cast<uint32_t *>(codes + t * (kTileElems / 2))[threadIdx.x] = c;
+    __builtin_nontemporal_store(c, reinterpret_cast<uint32_t *>(codes + t * (kTileElems / 2)) + threadIdx.x);
     if (threadIdx.x % 4 == 0)
         scales[t * kMxTileBlocks + threadIdx.x / 4] = uint8_t(s);
 }
 
-// The same for a lane's quad h of tile t, whose blocks are 8 lanes: 16 bits of
-// codes a lane.
-__device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t t, int h, const float x[4]) {
+// The same for a lane's quad, whose blocks are 8 lanes: 16 bits of codes.
+__device__ __forceinline__ void round_quad(const float x[4], uint32_t &codes, uint32_t &byte) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -178,14 +179,20 @@ __device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t
     top = max_quad(top);
     // the other quad of the 8 lanes: the mirror image within them
     top = max_bits(top, uint32_t(__builtin_amdgcn_mov_dpp(int(top), 0x141, 0xf, 0xf, true)));
-    const uint32_t ex = top >> 23, byte = ex == 255 ? 255 : ex > 2 ? ex - 2 : 0;
+    const uint32_t ex = top >> 23;
+    byte = ex == 255 ? 255 : ex > 2 ? ex - 2 : 0;
     const float s = scale_f32(byte);
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], s, 0);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
-    reinterpret_cast<uint16_t *>(codes + t * (kTileElems / 2))[64 * h + threadIdx.x] = ex == 255 ? 0 : uint16_t(c);
+    codes = ex == 255 ? 0 : c;
+}
+// Quad h of tile t: half words, which do better as plain stores (quantising
+// 1.2e8 elements with a residual: 208 us, 222 non-temporally).
+__device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t t, int h, uint32_t c, uint32_t s) {
+    reinterpret_cast<uint16_t *>(codes + t * (kTileElems / 2))[64 * h + threadIdx.x] = uint16_t(c);
     if (threadIdx.x % 8 == 0)
-        scales[t * kMxTileBlocks + 8 * h + threadIdx.x / 8] = uint8_t(byte);
+        scales[t * kMxTileBlocks + 8 * h + threadIdx.x / 8] = uint8_t(s);
 }
 
 // The sum of the contributions over the lane's 8 * kW slots of kW consecutive
@@ -444,8 +451,11 @@ __device__ __forceinline__ void step_whole(const MxStepArgs &a, const MxTile &t,
         if (a.param)
             __builtin_nontemporal_store(u32x2{to_bf16x2(p[0], p[1]), to_bf16x2(p[2], p[3])},
                                         reinterpret_cast<u32x2 *>(a.param + (a.param_local ? t.k : t.w) + at));
-        if (a.codes)
-            st_quad(a.codes, a.scales, a.mx_world ? t.world : t.local, h, p);
+        if (a.codes) {
+            uint32_t c, s;
+            round_quad(p, c, s);
+            st_quad(a.codes, a.scales, a.mx_world ? t.world : t.local, h, c, s);
+        }
     }
 }
 
@@ -536,100 +546,144 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4))) 
     }
 }
 
-// kMaster: the fp32 master; otherwise bf16 gradients, plus a residual if
-// there is one.
-template <bool kMaster, bool kWorld, bool kNT>
-__global__ __launch_bounds__(kBlock) void mx_quant_kernel(MxQuantArgs a) {
-    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const MxUnit u = unit_at<kWorld>(a.walk, i);
-        for (int j = 0; j < u.ntiles; ++j) {
-            const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
-            const Slots own = slots_of(t.lo, t.own);
-            const int64_t at = (a.local ? t.k : t.w) + threadIdx.x * kChunk;
+// ---- rounding to MXFP4 ---------------------------------------------------------------------------
+
+enum { kGrads, kGradsResidual, kMaster };   // what is rounded
+
+// A tile that is not whole, by chunks.
+template <int kSource>
+__device__ __forceinline__ void quant_edge(const MxQuantArgs &a, const MxTile &t) {
+    const Slots own = slots_of(t.lo, t.own);
+    const int64_t at = (a.local ? t.k : t.w) + threadIdx.x * kChunk;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = 0.0f;
+        if (e >= own.lo && e < own.hi) {
+            if constexpr (kSource == kMaster)
+                x[e] = a.master[at + e];
+            else
+                x[e] = h_f32(a.grads[at + e]);
+            if constexpr (kSource == kGradsResidual)
+                x[e] = x[e] + a.residual[at + e];
+        }
+    }
+    uint32_t c, s;
+    round_block(x, c, s);
+    st_block(a.codes, a.scales, a.world ? t.world : t.local, c, s);
+    if (kSource == kGradsResidual && s != 255) {
+        float y[8];
+        values_of(c, scale_f32(s), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= own.lo && e < own.hi)
+                a.residual[at + e] = x[e] - y[e];
+    }
+}
+
+// A unit of whole tiles from t: bf16 by chunks, fp32 by quads (and the bf16
+// beside it), so that every access covers a run without a gap; all loads
+// first. The fp32 is non-temporal, like the step's state (1.2e8 elements with
+// a residual 208 us, with plain accesses 257; the write-back of 1.25e8
+// elements 93 and 109 us). Tile by tile it took 212 and 96 us.
+template <int kSource>
+__device__ __forceinline__ void quant_whole(const MxQuantArgs &a, const MxTile &t) {
+    const int lane = int(threadIdx.x);
+    constexpr int kRun = kMxUnit;
+    const int64_t first = a.local ? t.k : t.w, to = a.world ? t.world : t.local;
+    if constexpr (kSource == kGrads) {
+        u32x4 r[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            r[j] = ld_rep(a.grads + first + j * kTileElems + lane * kChunk);
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) {
             float x[8];
-            if constexpr (kMaster) {
-                if (own.full()) {
-                    const f32x4 x0 = ld_state<kNT>(a.master + at), x1 = ld_state<kNT>(a.master + at + 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = x0[e];
-                        x[4 + e] = x1[e];
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = e >= own.lo && e < own.hi ? a.master[at + e] : 0.0f;
-                }
-            } else {
-                if (own.full()) {
-                    const u32x4 r = ld_rep(a.grads + at);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        x[2 * h] = lo_f32(r[h]);
-                        x[2 * h + 1] = hi_f32(r[h]);
-                    }
-                    if (a.residual) {
-                        const f32x4 r0 = ldf4(a.residual + at), r1 = ldf4(a.residual + at + 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = x[e] + r0[e];
-                            x[4 + e] = x[4 + e] + r1[e];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = 0.0f;
-                        if (e >= own.lo && e < own.hi) {
-                            x[e] = h_f32(a.grads[at + e]);
-                            if (a.residual)
-                                x[e] = x[e] + a.residual[at + e];
-                        }
-                    }
-                }
+            for (int h = 0; h < 4; ++h) {
+                x[2 * h] = lo_f32(r[j][h]);
+                x[2 * h + 1] = hi_f32(r[j][h]);
             }
             uint32_t c, s;
             round_block(x, c, s);
-            st_block(a.codes, a.scales, a.world ? t.world : t.local, c, s);
-            if (!kMaster && a.residual && s != 255) {
-                float y[8];
-                values_of(c, scale_f32(s), y);
+            st_block(a.codes, a.scales, to + j, c, s);
+        }
+    } else {
+        f32x4 f[2 * kRun];
+        u32x2 r[2 * kRun];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = x[e] - y[e];
-                if (own.full()) {
-                    stf4(a.residual + at, f32x4{y[0], y[1], y[2], y[3]});
-                    stf4(a.residual + at + 4, f32x4{y[4], y[5], y[6], y[7]});
-                } else {
+        for (int q = 0; q < 2 * kRun; ++q) {
+            const int64_t at = first + q * (kTileElems / 2) + 4 * lane;
+            f[q] = ld_state<true>(kSource == kMaster ? a.master + at : a.residual + at);
+            if constexpr (kSource == kGradsResidual)
+                r[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(a.grads + at));
+        }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e >= own.lo && e < own.hi)
-                            a.residual[at + e] = y[e];
-                }
+        for (int q = 0; q < 2 * kRun; ++q) {
+            float x[4] = {f[q][0], f[q][1], f[q][2], f[q][3]};
+            if constexpr (kSource == kGradsResidual) {
+                x[0] = lo_f32(r[q][0]) + x[0];
+                x[1] = hi_f32(r[q][0]) + x[1];
+                x[2] = lo_f32(r[q][1]) + x[2];
+                x[3] = hi_f32(r[q][1]) + x[3];
+            }
+            uint32_t c, s;
+            round_quad(x, c, s);
+            st_quad(a.codes, a.scales, to + q / 2, q % 2, c, s);
+            if (kSource == kGradsResidual && s != 255) {
+                const f32x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale_f32(s), 0);
+                const f32x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale_f32(s), 1);
+                st_state<true>(a.residual + first + q * (kTileElems / 2) + 4 * lane,
+                               f32x4{x[0] - y0[0], x[1] - y0[1], x[2] - y1[0], x[3] - y1[1]});
             }
         }
     }
 }
 
+template <int kSource, bool kWorld>
+__global__ __launch_bounds__(kBlock) void mx_quant_kernel(MxQuantArgs a) {
+    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
+        const MxUnit u = unit_at<kWorld>(a.walk, i);
+        const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile);
+        if (u.ntiles == kMxUnit && t.lo == 0 &&
+            tile_in(u.b, a.walk.dp, u.rank, u.tile + kMxUnit - 1).own == kTileElems) {
+            quant_whole<kSource>(a, t);
+            continue;
+        }
+        for (int j = 0; j < u.ntiles; ++j)
+            quant_edge<kSource>(a, tile_in(u.b, a.walk.dp, u.rank, u.tile + j));
+    }
+}
+
+// ---- the gather ------------------------------------------------------------------------------------
+
 __global__ __launch_bounds__(kBlock) void mx_gather_kernel(MxGatherArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
         const MxUnit u = unit_at<true>(a.walk, i);
         const uint8_t *codes = a.in.codes[u.rank], *scales = a.in.scales[u.rank];
+        const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile);
+        const int64_t at = stored_at(a.in, t);
         uint32_t c[kMxUnit], s[kMxUnit];
-        const MxTile t0 = tile_in(u.b, a.walk.dp, u.rank, u.tile);
-        const int64_t at = a.in.world ? t0.world : t0.local;
+        if (u.ntiles == kMxUnit && t.lo == 0 &&
+            tile_in(u.b, a.walk.dp, u.rank, u.tile + kMxUnit - 1).hi == kTileElems) {
 #pragma unroll
-        for (int j = 0; j < kMxUnit; ++j)
-            if (j < u.ntiles)
+            for (int j = 0; j < kMxUnit; ++j)
                 ld_block(codes, scales, at + j, c[j], s[j]);
 #pragma unroll
-        for (int j = 0; j < kMxUnit; ++j)
-            if (j < u.ntiles) {
-                const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
+            for (int j = 0; j < kMxUnit; ++j) {
                 float x[8];
                 values_of(c[j], scale_f32(s[j]), x);
-                st_bf16(a.out + t.w + threadIdx.x * kChunk, x, slots_of(t.lo, t.hi));
+                st_bf16(a.out + t.w + j * kTileElems + threadIdx.x * kChunk, x, {0, kChunk});
             }
+        } else {
+            for (int j = 0; j < u.ntiles; ++j) {
+                const MxTile e = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
+                ld_block(codes, scales, at + j, c[0], s[0]);
+                float x[8];
+                values_of(c[0], scale_f32(s[0]), x);
+                st_bf16(a.out + e.w + threadIdx.x * kChunk, x, slots_of(e.lo, e.hi));
+            }
+        }
     }
 }
 
@@ -729,27 +783,34 @@ hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t strea
     return hipGetLastError();
 }
 
-hipError_t launch_mx_quant(const MxQuantArgs &a, int lds_per_cu, hipStream_t stream) {
+// No cap on the waves: 1.2e8 elements 54 us (62 at 16 waves per compute unit),
+// 1e9 406 us (425 at 16), with a residual 208 us (206 at 12, 212 at 16).
+hipError_t launch_mx_quant(const MxQuantArgs &a, hipStream_t stream) {
     if (a.walk.count <= 0)
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
-    if (a.grads) {
-        if (a.local)
-            hipLaunchKernelGGL((mx_quant_kernel<false, false, false>), grid, block, 0, stream, a);
-        else
-            hipLaunchKernelGGL((mx_quant_kernel<false, true, false>), grid, block, 0, stream, a);
-    } else if (state_nontemporal(a.state_numel)) {
-        hipLaunchKernelGGL((mx_quant_kernel<true, false, true>), grid, block, 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((mx_quant_kernel<true, false, false>), grid, block, 0, stream, a);
-    }
+    if (!a.grads)
+        hipLaunchKernelGGL((mx_quant_kernel<kMaster, false>), grid, block, 0, stream, a);
+    else if (a.residual && a.local)
+        hipLaunchKernelGGL((mx_quant_kernel<kGradsResidual, false>), grid, block, 0, stream, a);
+    else if (a.residual)
+        hipLaunchKernelGGL((mx_quant_kernel<kGradsResidual, true>), grid, block, 0, stream, a);
+    else if (a.local)
+        hipLaunchKernelGGL((mx_quant_kernel<kGrads, false>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx_quant_kernel<kGrads, true>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
+
+// 20 waves per compute unit: 1e9 elements 408 us, 404 at 16, 547 at 8, 442
+// without a cap; 1.2e8 elements 52.6, 53.4, 70.4 and 54.9 us.
+constexpr int kMxGatherWaves = 20;
 
 hipError_t launch_mx_gather(const MxGatherArgs &a, int lds_per_cu, hipStream_t stream) {
     if (a.walk.count <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(mx_gather_kernel, dim3(grid_for(a.walk.count)), dim3(kBlock), 0, stream, a);
+    hipLaunchKernelGGL(mx_gather_kernel, dim3(grid_for(a.walk.count)), dim3(kBlock),
+                       lds_for_waves(lds_per_cu, kMxGatherWaves), stream, a);
     return hipGetLastError();
 }
 
