@@ -191,6 +191,8 @@ class Plan:
         n = ctypes.c_int32()
         _check(L.zdo_plan_buckets(h, None, 0, ctypes.byref(n)))
         self.num_buckets = int(n.value)
+        self._mx_blocks = tuple(int(L.zdo_plan_mx_blocks(h, c)) for c in (WORLD, LOCAL))
+        self.norm_mxfp4_workspace_bytes = int(L.zdo_plan_norm_mxfp4_workspace_bytes(h))
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -218,16 +220,11 @@ class Plan:
     def norm_workspace_bytes(self) -> int:
         return int(require_library().zdo_plan_norm_workspace_bytes(self.handle))
 
-    @property
-    def norm_mxfp4_workspace_bytes(self) -> int:
-        return int(require_library().zdo_plan_norm_mxfp4_workspace_bytes(self.handle))
-
     def mx_blocks(self, coords: int) -> int:
         """Blocks of the plan's MXFP4 storage in WORLD or LOCAL coordinates."""
-        n = int(require_library().zdo_plan_mx_blocks(self.handle, coords))
-        if n < 0:
+        if coords not in (WORLD, LOCAL):
             raise ValueError("coords must be WORLD or LOCAL")
-        return n
+        return self._mx_blocks[coords]
 
     def mx_buckets(self) -> np.ndarray:
         """Per bucket, its first block and its blocks in LOCAL storage (include/zdo_mx.h)."""
@@ -264,15 +261,24 @@ def _torch():
     return torch
 
 
+_DTYPES: dict = {}
+
+
+def _dtypes(kind: str):
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update(bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,),
+                       f64=(torch.float64,), bytes=(torch.uint8, torch.int8))
+    return _DTYPES[kind]
+
+
 def _dev_ptr(t, what: str, kind: str, numel: int | None) -> int:
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{what}: must be a device (cuda) tensor")
-    ok = {"bf16": (torch.bfloat16, torch.int16, torch.uint16), "f32": (torch.float32,),
-          "f64": (torch.float64,), "bytes": (torch.uint8, torch.int8)}[kind]
-    if t.dtype not in ok:
+    if t.dtype not in _dtypes(kind):
         raise TypeError(f"{what}: dtype {t.dtype} is not {kind}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")

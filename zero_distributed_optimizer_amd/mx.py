@@ -19,7 +19,7 @@ import ctypes
 
 import numpy as np
 
-from . import LOCAL, WORLD, Adam, Plan, _check, _dev_ptr, _stream, _torch, adam_hparams, require_library
+from . import LOCAL, WORLD, Adam, Plan, _check, _dev_ptr, _torch, adam_hparams, require_library
 
 MX_BUCKET_DTYPE = np.dtype([("block0", "<i8"), ("blocks", "<i8")])
 BLOCK = 32                # elements that share a scale
@@ -75,9 +75,9 @@ class MxBuffers:
             self.scales[j] = _dev_ptr(s, f"{what}[{j}] scales", "bytes", None)
             self.blocks = min(self.blocks, c.numel() // CODE_BYTES, s.numel())
             for t in (c, s):
-                if self.device is not None and t.device != self.device:
-                    raise ValueError(f"{what}[{j}]: on {t.device}, the others on {self.device}")
-                self.device = t.device
+                if self.device is not None and t.get_device() != self.device:
+                    raise ValueError(f"{what}[{j}]: on {t.device}, others on device {self.device}")
+                self.device = t.get_device()
 
     def __len__(self) -> int:
         return len(self.storages)
@@ -90,33 +90,34 @@ class MxBuffers:
 
 
 class _Call:
-    """One call's tensors: all on one device, which is the current one (the
-    plan's, as the library checks)."""
+    """Checks and marshals one call's tensors, which all live on the current
+    device (the plan's, as the library checks)."""
+
+    __slots__ = ("plan", "device")
 
     def __init__(self, plan: Plan):
         self.plan, self.device = plan, None
 
-    def on(self, device, what: str) -> None:
+    def on(self, device: int, what: str) -> None:
         if self.device is None:
-            self.device = device
-            if device.type == "cuda" and device.index != _torch().cuda.current_device():
-                raise ValueError(f"{what}: on {device}, which is not the current device")
-        elif device != self.device:
-            raise ValueError(f"{what}: on {device}, other tensors of the call on {self.device}")
+            self.device = _torch().cuda.current_device()
+        if device != self.device:
+            raise ValueError(f"{what}: on device {device}, but device {self.device} is current")
 
     def ptr(self, t, what: str, kind: str, numel: int):
         if t is None:
             return None
         p = _dev_ptr(t, what, kind, numel)
-        self.on(t.device, what)
+        if t.get_device() != self.device:
+            self.on(t.get_device(), what)
         return p
 
     def inputs(self, storages, what: str, coords: int) -> MxBuffers:
         mx = storages if isinstance(storages, MxBuffers) else MxBuffers(storages, what)
-        need = self.plan.mx_blocks(coords)
-        if mx.blocks < need and len(mx):
-            raise ValueError(f"{what}: needs at least {need} blocks per storage, has {mx.blocks}")
-        if len(mx):
+        if len(mx.storages):
+            need = self.plan.mx_blocks(coords)
+            if mx.blocks < need:
+                raise ValueError(f"{what}: needs at least {need} blocks per storage, has {mx.blocks}")
             self.on(mx.device, what)
         return mx
 
@@ -128,7 +129,10 @@ class _Call:
                 self.ptr(mx[1], f"{what} scales", "bytes", n))
 
     def stream(self, stream) -> int:
-        return _stream(stream, self.device)
+        # torch.cuda.current_stream builds a Stream object, 1.9 us; this reads its handle alone
+        if stream is None:
+            return _torch()._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream
 
     def buckets(self, buckets):
         if buckets is None:
