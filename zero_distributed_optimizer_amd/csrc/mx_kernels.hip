@@ -399,6 +399,40 @@ void mx_norm_wide_kernel(MxNormArgs a) {
     }
 }
 
+// Up to kSumOnce partials added by one workgroup: work-item t takes partials
+// t, t + 1024, ..., all loads first, then a fixed butterfly over each wave
+// and the 16 waves' sums in order. One launch where the two levels of longer
+// lists take two (fragmented step, clipped, 9410 tiles: 49.1 and 51.3 us; 32 a
+// work-item gain nothing).
+constexpr int kSumItems = 1024, kSumEach = 16;
+constexpr int64_t kSumOnce = kSumItems * kSumEach;
+__global__ __launch_bounds__(kSumItems) void mx_sum_kernel(const double *partial, int64_t n, double *out) {
+    __shared__ double waves[kSumItems / 64];
+    double x[kSumEach];
+#pragma unroll
+    for (int j = 0; j < kSumEach; ++j) {
+        const int64_t i = int64_t(j) * kSumItems + threadIdx.x;
+        x[j] = i < n ? partial[i] : 0.0;
+    }
+    double s = x[0];
+#pragma unroll
+    for (int j = 1; j < kSumEach; ++j)
+        s = s + x[j];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        s = s + __shfl_xor(s, off, 64);
+    if (threadIdx.x % 64 == 0)
+        waves[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = waves[0];
+#pragma unroll
+        for (int w = 1; w < kSumItems / 64; ++w)
+            t = t + waves[w];
+        *out = t;
+    }
+}
+
 // ---- the step --------------------------------------------------------------------------------
 // The state is read and rewritten once and a training step finds it cold:
 // its accesses are non-temporal (GPT-2 small rank, 187 MB of state, three
@@ -752,6 +786,10 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, int lds_per_c
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
+    }
+    if (a.walk.count <= kSumOnce) {
+        hipLaunchKernelGGL(mx_sum_kernel, dim3(1), dim3(kSumItems), 0, stream, a.partial, a.walk.count, norm_sq);
+        return hipGetLastError();
     }
     return launch_tile_sums(a.partial, a.walk.count, norm_sq, stream);
 }
