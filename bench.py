@@ -48,7 +48,7 @@ PEAK_HBM_GBPS = 8000.0
 STATE_CACHE_BYTES = 1 << 30      # below this, a back-to-back step finds state in the Infinity Cache
 CPU_CHUNK = 1 << 26
 KERNEL_SOURCES = [os.path.join(ROOT, "zero_distributed_optimizer_amd", "csrc", f)
-                  for f in ("kernels.hip", "kernels.h", "zdo_internal.h")]
+                  for f in ("kernels.hip", "device.h", "kernels.h", "zdo_internal.h")]
 
 
 def log(msg: str) -> None:

@@ -13,6 +13,7 @@ struct MxWalk {
     const uint32_t *group;  // the bucket of every kTileGroup-th LOCAL tile or unit
     int32_t nbuckets;
     int32_t dp, rank;
+    int32_t by_xcd;         // 8 consecutive tiles to an XCD (the launchers set it)
     int64_t first, count;
 };
 

@@ -72,15 +72,14 @@ __device__ __forceinline__ MxTile local_tile(const MxWalk &wk, int64_t i) {
     return tile_in(b, wk.dp, wk.rank, int(x - b->tile0));
 }
 
-// The walk index that launch slot i takes. As in the bf16 kernels, a short
-// launch hands each of the 8 XCDs 8 consecutive tiles out of every 64: those
-// 8 tiles' scales are one 128-byte line of every contribution. Measured with
-// and without: step, GPT-2 small rank 80.3 and 82.7 us, 64 contributions of
-// 1e7 elements 107.4 and 109.5 us; long launches are slower with it
-// (Llama-3-8B rank 4993 and 4976 us) and keep the dispatch order.
+// The walk index that launch slot i takes. With `by_xcd`, as in the bf16
+// kernels' short launches, each of the 8 XCDs takes 8 consecutive tiles out of
+// every 64: those 8 tiles' scales are one 128-byte line of every contribution,
+// which 8 XCDs would each fetch into their own L2 otherwise (1.11 times the
+// bytes that a step with 8 contributions needs).
 constexpr int64_t kShortLaunch = int64_t(1) << 17;
-__device__ __forceinline__ int64_t launch_order(int64_t count, int64_t i) {
-    if (count >= kShortLaunch || i >= count / 64 * 64)
+__device__ __forceinline__ int64_t launch_order(bool by_xcd, int64_t count, int64_t i) {
+    if (!by_xcd || i >= count / 64 * 64)
         return i;
     const int64_t r = i % 64;
     return i - r + (r % 8) * 8 + r / 8;
@@ -299,7 +298,7 @@ __device__ __forceinline__ void reduce_tile(const MxReduceArgs &a, const MxTile 
 // Short launches: a tile a wave, for the most waves.
 __global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x)
-        reduce_tile(a, local_tile(a.walk, launch_order(a.walk.count, i)));
+        reduce_tile(a, local_tile(a.walk, launch_order(a.walk.by_xcd, a.walk.count, i)));
 }
 
 // Long ones: a unit a wave, kW tiles at a time, so that a load instruction
@@ -374,7 +373,7 @@ __device__ __forceinline__ void put_partial(double *at, double s) {
 // As the reductions: one partial a tile, or a unit.
 __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const int64_t x = launch_order(a.walk.count, i);
+        const int64_t x = launch_order(a.walk.by_xcd, a.walk.count, i);
         put_partial(a.partial + x, norm_tile(a, local_tile(a.walk, x), 0.0));
     }
 }
@@ -572,7 +571,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4))) 
     const float cf = clip ? *ro(a.coeff) : 1.0f;
     const int64_t iend = clip && cf != cf ? 0 : a.walk.count;   // NaN: found-inf, nothing changes
     for (int64_t i = blockIdx.x; i < iend; i += gridDim.x) {
-        const MxTile t = local_tile(a.walk, launch_order(a.walk.count, i));
+        const MxTile t = local_tile(a.walk, launch_order(a.walk.by_xcd, a.walk.count, i));
         if (t.lo == 0 && t.own == kTileElems)
             step_whole<kN>(a, t, clip, cf, sums);
         else
@@ -758,6 +757,8 @@ hipError_t launch_mx_reduce(const MxReduceArgs &args, int lds_per_cu, hipStream_
     const ReduceForm f = reduce_form(a.in.n, a.walk.count);
     if (f.tiles > 1)
         a.walk = args.units;
+    else
+        a.walk.by_xcd = 1;
     if (a.walk.count <= 0)
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
@@ -775,6 +776,8 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, int lds_per_c
     const ReduceForm f = reduce_form(a.in.n, a.walk.count);
     if (f.tiles > 1)
         a.walk = args.units;
+    else
+        a.walk.by_xcd = 1;
     if (a.walk.count > 0) {
         const dim3 grid(grid_for(a.walk.count)), block(kBlock);
         const unsigned lds = reserve(lds_per_cu, f.waves, 0);
@@ -795,17 +798,23 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, int lds_per_c
 }
 
 // Waves that share a compute unit in the step. Long launches, Llama-3-8B
-// shapes: 8 contributions with all loads in flight 4958 us at 9 waves (8:
-// 4961, 10: 4982, 12: 5075, 6: 5926; in batches 5041 at 12), 16 2898 us (10:
-// 3014; in batches 3027); other counts 14 (3 contributions: 1331, at 12 1342
-// and at 16 1381; 32: 1854, 1850 and 1847; 12: 845, 860 and 840). Short
-// launches take 16 (GPT-2 small rank: the same from 10 up; fragmented, 16
-// contributions: 34.6 us, 36.3 at 10).
+// shapes: 8 contributions with all loads in flight 4809 us at 9 waves (8:
+// 4802, 10: 5227, 12: 5404, 6: 5901), 16 2871 us (8: 2875, 12: 2882); other
+// counts 14 (3 contributions: 1331, at 12 1342 and at 16 1381; 32: 1828, 1826
+// and 1838; 12: 812, 814 and 820). Short launches take 16 (GPT-2 small rank:
+// the same from 10 up; fragmented, 16 contributions: 34.6 us, 36.3 at 10).
+// Tiles go by XCD in short launches (GPT-2 small rank 80.3 us, 82.7 in
+// dispatch order; 64 contributions of 1e7 elements 107.4 and 109.5) and from 8
+// contributions in long ones, where the scales weigh enough (8: 4800 us, 4975
+// in dispatch order; 12: 813 and 847; 16: 2887 and 3062; 32: 1819 and 1893; but
+// 5: 716 and 718, 3: 1402 and 1381, 1: 1347 and 1311).
 constexpr int kStepWavesFixed = 9, kStepWaves = 14, kStepWavesShort = 16;
 
-hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t stream) {
-    if (a.walk.count <= 0)
+hipError_t launch_mx_step(const MxStepArgs &args, int lds_per_cu, hipStream_t stream) {
+    if (args.walk.count <= 0)
         return hipSuccess;
+    MxStepArgs a = args;
+    a.walk.by_xcd = a.walk.count < kShortLaunch || a.in.n >= 8;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
     const bool fixed = a.in.n == 8 || a.in.n == 16;
     const unsigned lds = reserve(lds_per_cu,
