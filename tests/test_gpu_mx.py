@@ -126,6 +126,46 @@ def test_quantize_every_bf16_at_every_phase(gpu):
     free()
 
 
+@pytest.mark.parametrize("D", [1, 3])
+@pytest.mark.parametrize("coords", [0, 1])
+def test_quantize_whole_units(either, D, coords):
+    """Ranges of many whole units beside their cut ends, with Inf and NaN in
+    some blocks, with and without a residual."""
+    gpu, rng = either, np.random.default_rng(D)
+    sizes, bucket = [50_000, 33, 70_001, 8192, 4096, 2048], 60_000
+    lay = OL.build_layout(sizes, bucket, D)
+    n = lay.buffer_numel if coords == gpu.WORLD else OL.shard_numel(lay, D - 1)
+    g = bf16_host(rng, n)
+    g[rng.integers(0, n, 20)] = 0x7F80
+    g[rng.integers(0, n, 20)] = 0xFFC1
+    check_quantize(gpu, sizes, bucket, D, D - 1, coords, g)
+    check_quantize(gpu, sizes, bucket, D, D - 1, coords, g, (rng.standard_normal(n) * 1e-3).astype(np.float32))
+    free()
+
+
+@pytest.mark.parametrize("coords", [0, 1])
+def test_parameters_of_whole_units(either, coords):
+    gpu, rng = either, np.random.default_rng(7)
+    sizes, bucket, D = [50_000, 33, 70_001, 8192], 60_000, 3
+    lay = OL.build_layout(sizes, bucket, D)
+    want, got = [], []
+    for r in range(D):
+        plan = gpu.build_range_map(sizes, bucket, D, r)
+        m = (rng.standard_normal(plan.shard_numel) * 0.02).astype(np.float32)
+        m[rng.integers(0, m.size, 5)] = np.inf
+        want.append(MX.empty(lay, coords, FILL))
+        got.append(dev_mx(want[-1]))
+        MX.writeback(lay, r, m, want[-1], coords)
+        gpu.writeback_params_mxfp4(plan, to_dev(m), got[-1], coords)
+        assert_mx(got[-1], want[-1], f"write-back r={r}")
+    out = torch.full((lay.buffer_numel,), SENTINEL, dtype=torch.int16, device=DEV)
+    ref = np.full(lay.buffer_numel, SENTINEL, np.uint16)
+    gpu.all_gather_params_mxfp4(plan, got, coords, out)
+    MX.all_gather(lay, want, coords, ref)
+    assert_bf16(host_u16(out), ref, "gather")
+    free()
+
+
 def test_residual_of_a_block_that_is_not_finite_stays(gpu):
     n = 1000
     rng = np.random.default_rng(0)
@@ -746,6 +786,13 @@ def test_refusals(gpu):
         gpu.quantize_grads_mxfp4(plan, g[:8], gpu.WORLD, world)
     with pytest.raises(TypeError):
         gpu.quantize_grads_mxfp4(plan, g.float(), gpu.WORLD, world)
+    for missing in (None, (world[0],), (world[0], None)):
+        with pytest.raises(TypeError):
+            gpu.quantize_grads_mxfp4(plan, g, gpu.WORLD, missing)
+    with pytest.raises(TypeError):
+        gpu.quantize_grads_mxfp4(plan, None, gpu.WORLD, world)
+    with pytest.raises(TypeError):
+        gpu.sharded_adam_step_mxfp4(plan, [local], gpu.LOCAL, 1.0, f[0], None, f[2], **hp)
     with pytest.raises(ValueError, match="contiguous"):
         gpu.MxBuffers([(world[0].t(), world[1])])
     with pytest.raises(ValueError, match="device"):

@@ -104,13 +104,14 @@ class _Call:
         if device != self.device:
             raise ValueError(f"{what}: on device {device}, but device {self.device} is current")
 
-    def ptr(self, t, what: str, kind: str, numel: int):
-        if t is None:
-            return None
+    def ptr(self, t, what: str, kind: str, numel: int) -> int:
         p = _dev_ptr(t, what, kind, numel)
         if t.get_device() != self.device:
             self.on(t.get_device(), what)
         return p
+
+    def opt(self, t, what: str, kind: str, numel: int):
+        return None if t is None else self.ptr(t, what, kind, numel)
 
     def inputs(self, storages, what: str, coords: int) -> MxBuffers:
         mx = storages if isinstance(storages, MxBuffers) else MxBuffers(storages, what)
@@ -122,8 +123,8 @@ class _Call:
         return mx
 
     def storage(self, mx, what: str, coords: int):
-        if mx is None:
-            return None, None
+        if mx is None or len(mx) != 2:
+            raise TypeError(f"{what}: expected a storage, a pair (codes, scales)")
         n = self.plan.mx_blocks(coords)
         return (self.ptr(mx[0], f"{what} codes", "bytes", CODE_BYTES * n),
                 self.ptr(mx[1], f"{what} scales", "bytes", n))
@@ -132,6 +133,7 @@ class _Call:
         # torch.cuda.current_stream builds a Stream object, 1.9 us; this reads its handle alone
         if stream is None:
             return _torch()._C._cuda_getCurrentRawStream(self.device)
+        self.on(stream.device.index, "stream")
         return stream.cuda_stream
 
     def buckets(self, buckets):
@@ -147,7 +149,7 @@ def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buc
     buckets only."""
     call, n = _Call(plan), plan.extent(coords)
     g = call.ptr(grads, "grads", "bf16", n)
-    r = call.ptr(residual, "residual", "f32", n)
+    r = call.opt(residual, "residual", "f32", n)
     c, s = call.storage(out, "out", coords)
     b0, b1 = call.buckets(buckets)
     _check(require_library().quantize_grads_mxfp4(plan.handle, b0, b1, g, coords, r, c, s, call.stream(stream)))
@@ -194,10 +196,10 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     m = call.ptr(master, "master", "f32", L)
     a = call.ptr(exp_avg, "exp_avg", "f32", L)
     v = call.ptr(exp_avg_sq, "exp_avg_sq", "f32", L)
-    p = None if param_out is None else call.ptr(param_out, "param_out", "bf16", plan.extent(param_coords))
-    pc, ps = call.storage(param_mx, "param_mx", param_mx_coords)
-    gc = call.ptr(grad_coeff, "grad_coeff", "f32", 1)
-    mg = call.ptr(main_grad_out, "main_grad_out", "f32", L)
+    p = call.opt(param_out, "param_out", "bf16", plan.extent(param_coords))
+    pc, ps = (None, None) if param_mx is None else call.storage(param_mx, "param_mx", param_mx_coords)
+    gc = call.opt(grad_coeff, "grad_coeff", "f32", 1)
+    mg = call.opt(main_grad_out, "main_grad_out", "f32", L)
     hp = adam_hparams(lr, beta1, beta2, eps, weight_decay, step)
     b0, b1 = call.buckets(buckets)
     _check(require_library().sharded_adam_step_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale,
