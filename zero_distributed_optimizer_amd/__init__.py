@@ -323,9 +323,11 @@ def _ptr_list(ts, what: str, numel: int):
 
 
 def _stream(stream, device) -> int:
-    torch = _torch()
+    """The handle of `stream`, or of the current stream of `device` (a device
+    or its index), read by itself: torch.cuda.current_stream builds a Stream
+    object, which takes 1.9 us."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return _torch()._C._cuda_getCurrentRawStream(device if isinstance(device, int) else device.index)
     return stream.cuda_stream
 
 

@@ -19,7 +19,7 @@ import ctypes
 
 import numpy as np
 
-from . import LOCAL, WORLD, Adam, Plan, _check, _dev_ptr, _torch, adam_hparams, require_library
+from . import LOCAL, WORLD, Adam, Plan, _check, _dev_ptr, _stream, _torch, adam_hparams, require_library
 
 MX_BUCKET_DTYPE = np.dtype([("block0", "<i8"), ("blocks", "<i8")])
 BLOCK = 32                # elements that share a scale
@@ -70,7 +70,12 @@ class MxBuffers:
         n = len(self.storages)
         self.codes, self.scales = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
         self.blocks, self.device = (1 << 62 if n else 0), None
+        before = (None, None)
         for j, (c, s) in enumerate(self.storages):
+            if c is before[0] and s is before[1]:   # the same storage again, as the gather may be given it
+                self.codes[j], self.scales[j] = self.codes[j - 1], self.scales[j - 1]
+                continue
+            before = (c, s)
             self.codes[j] = _dev_ptr(c, f"{what}[{j}] codes", "bytes", None)
             self.scales[j] = _dev_ptr(s, f"{what}[{j}] scales", "bytes", None)
             self.blocks = min(self.blocks, c.numel() // CODE_BYTES, s.numel())
@@ -130,11 +135,9 @@ class _Call:
                 self.ptr(mx[1], f"{what} scales", "bytes", n))
 
     def stream(self, stream) -> int:
-        # torch.cuda.current_stream builds a Stream object, 1.9 us; this reads its handle alone
-        if stream is None:
-            return _torch()._C._cuda_getCurrentRawStream(self.device)
-        self.on(stream.device.index, "stream")
-        return stream.cuda_stream
+        if stream is not None:
+            self.on(stream.device.index, "stream")
+        return _stream(stream, self.device)
 
     def buckets(self, buckets):
         if buckets is None:
