@@ -10,8 +10,7 @@ namespace zdo {
 // count).
 struct MxWalk {
     const MxBucket *buckets;
-    const uint32_t *group;  // the bucket of every kTileGroup-th LOCAL tile or unit
-    int32_t nbuckets;
+    const uint32_t *group;  // the bucket of every kTileGroup-th LOCAL tile or unit, then the last bucket
     int32_t dp, rank;
     int32_t by_xcd;         // 8 consecutive tiles to an XCD (the launchers set it)
     int64_t first, count;

@@ -115,7 +115,6 @@ MxWalk walk_of(const zdo_plan *p, int32_t b0, int32_t b1, bool units, bool world
     MxWalk w{};
     w.buckets = p->d_mx_buckets;
     w.group = units ? p->d_mx_unit_group : p->d_mx_tile_group;
-    w.nbuckets = int32_t(p->mx_buckets.size());
     w.dp = p->dp_size;
     w.rank = p->rank;
     w.first = start(b0);

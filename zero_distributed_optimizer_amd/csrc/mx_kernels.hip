@@ -55,14 +55,23 @@ __device__ __forceinline__ MxTile tile_in(ro_ptr<MxBucket> b, int dp, int r, int
     return t;
 }
 
-// The bucket holding LOCAL tile or unit x.
+// The bucket holding LOCAL tile or unit x: the one that holds the first of
+// its group of kTileGroup, unless buckets start within the group; then by
+// halving (about 19,000 buckets of 2,100 elements at D = 4: step 64 us, 74 by
+// one bucket after the other; quantise with residual and back 264 and 308).
 template <bool kUnits>
 __device__ __forceinline__ ro_ptr<MxBucket> bucket_of(const MxWalk &wk, int64_t x) {
     const ro_ptr<MxBucket> all = ro(wk.buckets);
-    int32_t b = int32_t(ro(wk.group)[x / kTileGroup]);
-    while (b + 1 < wk.nbuckets && (kUnits ? all[b + 1].unit0 : all[b + 1].tile0) <= x)
-        ++b;
-    return all + b;
+    const ro_ptr<uint32_t> g = ro(wk.group) + x / kTileGroup;
+    uint32_t lo = g[0], hi = g[1];
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi + 1) / 2;
+        if ((kUnits ? all[mid].unit0 : all[mid].tile0) <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return all + lo;
 }
 
 // The tile at launch index i of a walk over the rank's tiles.

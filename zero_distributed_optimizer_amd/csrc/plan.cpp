@@ -189,12 +189,15 @@ int upload_plan(zdo_plan &p) {
     const auto range_group = group_segs(p.range_segs, p.range_tiles);
     const auto gather_group =
         group_index(p.gather_tiles, p.gather_ranges.size(), [&](size_t y) { return p.gather_ranges[y].tile0; });
-    // the MXFP4 walks' index; a plan that the MXFP4 calls refuse has none
+    // the MXFP4 walks' index, with the last bucket behind it; a plan that the
+    // MXFP4 calls refuse has none
     const bool mx = p.mx_tiles <= kMxMaxTiles;
-    const auto mx_tile_group = group_index(mx ? p.mx_tiles : 0, p.mx_buckets.size(),
-                                           [&](size_t y) { return p.mx_buckets[y].tile0; });
-    const auto mx_unit_group = group_index(mx ? p.mx_units : 0, p.mx_buckets.size(),
-                                           [&](size_t y) { return p.mx_buckets[y].unit0; });
+    auto mx_tile_group = group_index(mx ? p.mx_tiles : 0, p.mx_buckets.size(),
+                                     [&](size_t y) { return p.mx_buckets[y].tile0; });
+    auto mx_unit_group = group_index(mx ? p.mx_units : 0, p.mx_buckets.size(),
+                                     [&](size_t y) { return p.mx_buckets[y].unit0; });
+    mx_tile_group.push_back(uint32_t(p.mx_buckets.size() - 1));
+    mx_unit_group.push_back(uint32_t(p.mx_buckets.size() - 1));
     // one allocation: segments, the two walks' group entries, the gather
     // ranges, the MXFP4 buckets, then the gather's and the MXFP4 walks' index
     const size_t nseg = p.param_segs.size() + p.range_segs.size();
