@@ -61,7 +61,8 @@ int64_t zdo_plan_mx_blocks(const zdo_plan *plan, int32_t coords);
 /* Two-call query as zdo_plan_buckets. */
 int zdo_plan_mx_buckets(const zdo_plan *plan, zdo_mx_bucket *out, int32_t cap, int32_t *n);
 
-/* Workspace bytes grad_norm_sq_mxfp4 needs: 8 per LOCAL tile plus 8 KiB. */
+/* Workspace bytes grad_norm_sq_mxfp4 needs: 8 per LOCAL tile, 128 KiB at
+ * most. */
 int64_t zdo_plan_norm_mxfp4_workspace_bytes(const zdo_plan *plan);
 
 /* A gradient buffer to MXFP4, for the buckets [bucket_begin, bucket_end): the
@@ -95,10 +96,10 @@ int reduce_scatter_local_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32
 
 /* The squared norm of the gradient that sharded_adam_step_mxfp4 steps with:
  * sum of g^2 over the rank's owned parameter elements, g = scale * (x_0 + x_1
- * + ...) in fp32 as above, squares (exact) and sums in fp64, in an order that
- * depends on the plan and n only: per run of 1 or up to 4 tiles (a lane's
- * slots in order, then a fixed butterfly over 64 lanes) into `workspace`,
- * then grad_norm_sq's two levels.
+ * + ...) in fp32 as above, squares (exact) and sums in fp64, in a fixed order
+ * that depends on the plan and n only, so that equal inputs give equal bits:
+ * each wave of the launch adds its tiles' squares into `workspace`, then the
+ * waves' sums are added.
  * workspace: zdo_plan_norm_mxfp4_workspace_bytes(plan) bytes, 16-byte
  * aligned, this call's alone until it completes. norm_sq_out: device double.
  * A rank that owns nothing gets 0. A block with scale 255 makes it NaN, and

@@ -32,7 +32,7 @@ hipError_t no_alloc_scratch(void **out) { *out = nullptr; return hipErrorNoDevic
 hipError_t launch_probe(const ProbeArgs &, int, int, hipStream_t) { return hipErrorNoDevice; }
 static hipError_t seen(const MxWalk &w) { ++launches; last = w; return hipSuccess; }
 hipError_t launch_mx_reduce(const MxReduceArgs &a, int, hipStream_t) { return seen(a.walk); }
-hipError_t launch_mx_norm(const MxNormArgs &a, double *, int, hipStream_t) { return seen(a.walk); }
+hipError_t launch_mx_norm(const MxNormArgs &a, double *, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_step(const MxStepArgs &a, int, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_quant(const MxQuantArgs &a, hipStream_t) { return seen(a.walk); }
 hipError_t launch_mx_gather(const MxGatherArgs &a, int, hipStream_t) { return seen(a.walk); }

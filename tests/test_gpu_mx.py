@@ -731,10 +731,13 @@ def test_loops_beyond_the_grid(gpu):
     want = np.zeros(loop.N, np.uint16)
     MX.reduce_scatter(loop.lay, 1, [host_mx(c) for c in ref["con"]], MX.WORLD, 0.25, want, MX.WORLD)
     assert_bf16(host_u16(red), want, "reduce-scatter")
+    assert torch.equal(d["coeff"], ref["coeff"])   # else the steps below differ
     for k in ("st", "con", "par"):
         for a, b in zip(d[k], ref[k]):
             assert all(torch.equal(x, y) for x, y in zip(a, b)), k
-    assert torch.equal(d["out"], ref["out"]) and torch.equal(d["parts"], ref["parts"])
+    assert torch.equal(d["out"], ref["out"])
+    for r in range(D):   # the waves of the two builds, and so the order of their sums, differ
+        assert_norm(float(d["parts"][r]), float(ref["parts"][r]), loop.plans[r].owned_numel, f"norm {r}")
     free()
 
 

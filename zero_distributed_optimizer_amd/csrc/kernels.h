@@ -134,9 +134,6 @@ hipError_t launch_gather(const GatherArgs &a, int lds_per_cu, hipStream_t stream
 // Squared norm: per-tile partials into a.partial, then their fixed-order sum
 // into *norm_sq (0 when a.walk has no tiles).
 hipError_t launch_norm(const NormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream);
-// The second half of the squared norm: n tile partials (with room for 1024
-// doubles after them) added in two fixed-order levels into *norm_sq.
-hipError_t launch_tile_sums(double *partial, int64_t n, double *norm_sq, hipStream_t stream);
 hipError_t launch_clip(const double *parts, int32_t n, float max_norm, float *coeff, double *norm_out,
                        hipStream_t stream);
 // Device address of the library's static scratch array on the current

@@ -931,20 +931,6 @@ hipError_t launch_writeback(const WritebackArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_tile_sums(double *partial, int64_t n, double *norm_sq, hipStream_t stream) {
-    // level 1: G <= kSumGroups runs of `chunk` partials; level 2: one workgroup
-    int64_t g = (n + kSumThreads - 1) / kSumThreads;
-    if (g > kSumGroups)
-        g = kSumGroups;
-    if (g < 1)
-        g = 1;
-    const int64_t chunk = n > 0 ? (n + g - 1) / g : 1;
-    double *level = partial + (n > 0 ? n : 0);
-    hipLaunchKernelGGL(tile_sum_kernel, dim3(unsigned(g)), dim3(kSumThreads), 0, stream, partial, n, chunk, level);
-    hipLaunchKernelGGL(level_sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, level, g, norm_sq);
-    return hipGetLastError();
-}
-
 hipError_t launch_norm(const NormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream) {
     if (a.walk.ntiles > 0) {
         const dim3 grid(grid_for(a.walk.ntiles)), block(kBlock);
@@ -962,7 +948,18 @@ hipError_t launch_norm(const NormArgs &a, double *norm_sq, int lds_per_cu, hipSt
         if (e != hipSuccess)
             return e;
     }
-    return launch_tile_sums(a.partial, a.walk.ntiles, norm_sq, stream);
+    // level 1: G <= kSumGroups runs of `chunk` partials; level 2: one workgroup
+    const int64_t n = a.walk.ntiles;
+    int64_t g = (n + kSumThreads - 1) / kSumThreads;
+    if (g > kSumGroups)
+        g = kSumGroups;
+    if (g < 1)
+        g = 1;
+    const int64_t chunk = n > 0 ? (n + g - 1) / g : 1;
+    double *level = a.partial + (n > 0 ? n : 0);
+    hipLaunchKernelGGL(tile_sum_kernel, dim3(unsigned(g)), dim3(kSumThreads), 0, stream, a.partial, n, chunk, level);
+    hipLaunchKernelGGL(level_sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, level, g, norm_sq);
+    return hipGetLastError();
 }
 
 namespace {

@@ -32,11 +32,14 @@ struct MxReduceArgs {
     uint16_t *out;
 };
 
+// Most waves of a squared norm, each of which leaves one sum.
+constexpr int64_t kMxNormWaves = 16384;
+
 struct MxNormArgs {
     MxWalk walk, units;  // LOCAL tiles, and units
     MxInputs in;
     float scale;
-    double *partial;  // one per tile or unit
+    double *partial;  // one per wave
 };
 
 struct MxStepArgs {
@@ -70,7 +73,7 @@ struct MxGatherArgs {
 };
 
 hipError_t launch_mx_reduce(const MxReduceArgs &a, int lds_per_cu, hipStream_t stream);
-hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, int lds_per_cu, hipStream_t stream);
+hipError_t launch_mx_norm(const MxNormArgs &a, double *norm_sq, hipStream_t stream);
 hipError_t launch_mx_step(const MxStepArgs &a, int lds_per_cu, hipStream_t stream);
 hipError_t launch_mx_quant(const MxQuantArgs &a, hipStream_t stream);
 hipError_t launch_mx_gather(const MxGatherArgs &a, int lds_per_cu, hipStream_t stream);

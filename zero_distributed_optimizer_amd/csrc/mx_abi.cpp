@@ -2,6 +2,7 @@
 // documented in include/zdo_mx.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <new>
 #include <string>
@@ -154,8 +155,8 @@ int zdo_plan_mx_buckets(const zdo_plan *p, zdo_mx_bucket *out, int32_t cap, int3
 int64_t zdo_plan_norm_mxfp4_workspace_bytes(const zdo_plan *p) {
     if (!p)
         return -1;
-    // one partial per tile, then up to 1024 second-level sums
-    return (p->mx_tiles + 1024) * int64_t(sizeof(double));
+    // one sum per wave, of at most one a tile
+    return std::min(p->mx_tiles, kMxNormWaves) * int64_t(sizeof(double));
 }
 
 int quantize_grads_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32_t bucket_end, const uint16_t *grads,
@@ -246,7 +247,7 @@ int grad_norm_sq_mxfp4(const zdo_plan *plan, const uint8_t *const *codes, const 
         a.units = walk_of(plan, 0, nbuckets(plan), true, false);
         a.scale = scale;
         a.partial = static_cast<double *>(workspace);
-        return launch_result(launch_mx_norm(a, norm_sq_out, plan->lds_per_cu, static_cast<hipStream_t>(stream)), fn);
+        return launch_result(launch_mx_norm(a, norm_sq_out, static_cast<hipStream_t>(stream)), fn);
     });
 }
 

@@ -33,7 +33,6 @@ struct MxTile {
     int64_t w, k;     // WORLD and LOCAL index of its slot 0 (k: the plan's rank only)
     int lo, hi, own;  // its slots [lo, hi) lie in the range, [lo, own) are parameter elements
     int64_t local, world;  // its number in LOCAL and in WORLD storage
-    int rank;
 };
 
 __device__ __forceinline__ int clamp_slot(int64_t x) { return x < 0 ? 0 : x > kTileElems ? kTileElems : int(x); }
@@ -51,7 +50,6 @@ __device__ __forceinline__ MxTile tile_in(ro_ptr<MxBucket> b, int dp, int r, int
     t.own = clamp_slot((oe < re ? oe : re) - t.w);
     t.local = b->tile0 + i;
     t.world = dp * b->tile0 + int64_t(r) * b->tiles + i;
-    t.rank = r;
     return t;
 }
 
@@ -211,11 +209,12 @@ __device__ __forceinline__ void st_quad(uint8_t *codes, uint8_t *scales, int64_t
 // block), in the order given, from -0 (which adds to any first term
 // exactly). kN > 0: that many contributions, all their loads in flight
 // together; kN = 0: any number, in batches of 16 and what is left, each
-// batch's loads in flight together. (A batch of the same code for any count up
+// batch's loads in flight together (kMost = kFew: fewer than 4, for which fewer
+// registers are enough and more waves fit). (A batch of the same code for any count up
 // to 16, its loads behind uniform branches, took 1.9 times as long at 16
 // contributions and 4 times at 32: the waits behind a branch are for every
 // load.)
-constexpr int kBatch = 16;
+constexpr int kBatch = 16, kFew = 4;
 template <int kW, int kCount>
 __device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t at, float acc[8 * kW]) {
     typedef unsigned int words __attribute__((ext_vector_type(kW)));
@@ -239,15 +238,17 @@ __device__ __forceinline__ void add_batch(const MxInputs &in, int j, int64_t at,
                 acc[8 * w + e] = acc[8 * w + e] + x[e];
         }
 }
-template <int kW, int kN>
+template <int kW, int kN, int kMost = kBatch>
 __device__ __forceinline__ void sum_blocks(const MxInputs &in, int64_t at, float acc[8 * kW]) {
 #pragma unroll
     for (int e = 0; e < 8 * kW; ++e)
         acc[e] = -0.0f;
     if constexpr (kN > 0) {
         add_batch<kW, kN>(in, 0, at, acc);
-    } else {
-        int j = 0;
+        return;
+    }
+    int j = 0;
+    if constexpr (kMost == kBatch) {
         for (; j + kBatch <= in.n; j += kBatch)
             add_batch<kW, kBatch>(in, j, at, acc);
         if (in.n & 8) {
@@ -255,15 +256,18 @@ __device__ __forceinline__ void sum_blocks(const MxInputs &in, int64_t at, float
             j += 8;
         }
         switch (in.n & 7) {
-        case 1: add_batch<kW, 1>(in, j, at, acc); break;
-        case 2: add_batch<kW, 2>(in, j, at, acc); break;
-        case 3: add_batch<kW, 3>(in, j, at, acc); break;
-        case 4: add_batch<kW, 4>(in, j, at, acc); break;
-        case 5: add_batch<kW, 5>(in, j, at, acc); break;
-        case 6: add_batch<kW, 6>(in, j, at, acc); break;
-        case 7: add_batch<kW, 7>(in, j, at, acc); break;
+        case 4: add_batch<kW, 4>(in, j, at, acc); return;
+        case 5: add_batch<kW, 5>(in, j, at, acc); return;
+        case 6: add_batch<kW, 6>(in, j, at, acc); return;
+        case 7: add_batch<kW, 7>(in, j, at, acc); return;
         default: break;
         }
+    }
+    switch (in.n & 3) {
+    case 1: add_batch<kW, 1>(in, j, at, acc); break;
+    case 2: add_batch<kW, 2>(in, j, at, acc); break;
+    case 3: add_batch<kW, 3>(in, j, at, acc); break;
+    default: break;
     }
 }
 __device__ __forceinline__ int64_t stored_at(const MxInputs &in, const MxTile &t) { return in.world ? t.world : t.local; }
@@ -319,8 +323,8 @@ __global__ __launch_bounds__(kBlock) void mx_reduce_kernel(MxReduceArgs a) {
 // that a store covers 1 KiB without a gap.
 __device__ __forceinline__ int chunk_place(int c) { return (c & ~7) | ((c ^ (c >> 3)) & 7); }
 
-template <int kW>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4)))
+template <int kW, int kMost>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, kMost < kBatch ? 8 : 4)))
 void mx_reduce_wide_kernel(MxReduceArgs a) {
     __shared__ u32x4 chunks[kBlock * kW];
     const int lane = int(threadIdx.x);
@@ -332,7 +336,7 @@ void mx_reduce_wide_kernel(MxReduceArgs a) {
             if (t.lo != 0 || tile_in(u.b, a.walk.dp, u.rank, u.tile + j + kW - 1).hi != kTileElems)
                 break;
             float acc[8 * kW];
-            sum_blocks<kW, 0>(a.in, stored_at(a.in, t), acc);
+            sum_blocks<kW, 0, kMost>(a.in, stored_at(a.in, t), acc);
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
                 u32x4 o;
@@ -355,24 +359,30 @@ void mx_reduce_wide_kernel(MxReduceArgs a) {
     }
 }
 
-// The squares of a lane's n slots, those of [lo, hi) only, added in order.
-template <int kSlots>
-__device__ __forceinline__ double add_squares(double s, const float acc[kSlots], float scale, int lo, int hi) {
+// The squares of a lane's slots, those of [lo, hi) only, into four running
+// sums by the slot's number modulo 4, which keeps the chain of fp64 additions
+// short. A square of an fp32 is exact in fp64, so the fused operation rounds
+// as an addition of it does.
+struct Squares {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    template <int kSlots>
+    __device__ __forceinline__ void add(const float acc[kSlots], float scale, int lo, int hi) {
 #pragma unroll
-    for (int e = 0; e < kSlots; ++e) {
-        const double g = double(acc[e] * scale);
-        if (e >= lo && e < hi)
-            s = s + g * g;
+        for (int e = 0; e < kSlots; ++e) {
+            const double g = double(acc[e] * scale);
+            if (e >= lo && e < hi)
+                s[e % 4] = __builtin_fma(g, g, s[e % 4]);
+        }
     }
-    return s;
-}
-__device__ __forceinline__ double norm_tile(const MxNormArgs &a, const MxTile &t, double s) {
+    __device__ __forceinline__ double total() const { return (s[0] + s[1]) + (s[2] + s[3]); }
+};
+__device__ __forceinline__ void norm_tile(const MxNormArgs &a, const MxTile &t, Squares &s) {
     if (t.lo >= t.own)
-        return s;
+        return;
     float acc[8];
     sum_blocks<1, 0>(a.in, stored_at(a.in, t), acc);
     const Slots own = slots_of(t.lo, t.own);
-    return add_squares<8>(s, acc, a.scale, own.lo, own.hi);
+    s.add<8>(acc, a.scale, own.lo, own.hi);
 }
 __device__ __forceinline__ void put_partial(double *at, double s) {
 #pragma unroll
@@ -382,41 +392,43 @@ __device__ __forceinline__ void put_partial(double *at, double s) {
         *at = s;
 }
 
-// As the reductions: one partial a tile, or a unit.
+// As the reductions, but with at most kMxNormWaves waves, each of which takes
+// every kMxNormWaves-th tile or unit and adds its lanes once at the end. A wave a
+// unit spent its time filling and in the butterfly: 3e8 slots of 1
+// contribution 62 us instead of 119, of 3 92 instead of 138, 5e8 of 16 663
+// instead of 694, GPT-2 small rank 19.7 instead of 21.9 (with 8192 waves
+// 64, 96, 668 and 19.8 us, with 4096 70, 99, 681 and 20.5).
 __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
-    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
-        const int64_t x = launch_order(a.walk.by_xcd, a.walk.count, i);
-        put_partial(a.partial + x, norm_tile(a, local_tile(a.walk, x), 0.0));
-    }
+    Squares s;
+    for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x)
+        norm_tile(a, local_tile(a.walk, launch_order(a.walk.by_xcd, a.walk.count, i)), s);
+    put_partial(a.partial + blockIdx.x, s.total());
 }
-template <int kW>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4)))
+template <int kW, int kMost>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, kMost < kBatch ? 8 : 4)))
 void mx_norm_wide_kernel(MxNormArgs a) {
+    Squares s;
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x) {
         const MxUnit u = unit_at<false>(a.walk, i);
-        double s = 0.0;
         int j = 0;
         for (; j + kW <= u.ntiles; j += kW) {
             const MxTile t = tile_in(u.b, a.walk.dp, u.rank, u.tile + j);
             if (t.lo != 0 || tile_in(u.b, a.walk.dp, u.rank, u.tile + j + kW - 1).own != kTileElems)
                 break;
             float acc[8 * kW];
-            sum_blocks<kW, 0>(a.in, stored_at(a.in, t), acc);
-            s = add_squares<8 * kW>(s, acc, a.scale, 0, 8 * kW);
+            sum_blocks<kW, 0, kMost>(a.in, stored_at(a.in, t), acc);
+            s.add<8 * kW>(acc, a.scale, 0, 8 * kW);
         }
         for (; j < u.ntiles; ++j)
-            s = norm_tile(a, tile_in(u.b, a.walk.dp, u.rank, u.tile + j), s);
-        put_partial(a.partial + i, s);
+            norm_tile(a, tile_in(u.b, a.walk.dp, u.rank, u.tile + j), s);
     }
+    put_partial(a.partial + blockIdx.x, s.total());
 }
 
-// Up to kSumOnce partials added by one workgroup: work-item t takes partials
-// t, t + 1024, ..., all loads first, then a fixed butterfly over each wave
-// and the 16 waves' sums in order. One launch where the two levels of longer
-// lists take two (fragmented step, clipped, 9410 tiles: 49.1 and 51.3 us; 32 a
-// work-item gain nothing).
-constexpr int kSumItems = 1024, kSumEach = 16;
-constexpr int64_t kSumOnce = kSumItems * kSumEach;
+// The waves' sums added by one workgroup: work-item t takes sums t, t + 1024,
+// ..., all loads first, then a fixed butterfly over each wave and the 16
+// waves' sums in order.
+constexpr int kSumItems = 1024, kSumEach = int(kMxNormWaves / kSumItems);
 __global__ __launch_bounds__(kSumItems) void mx_sum_kernel(const double *partial, int64_t n, double *out) {
     __shared__ double waves[kSumItems / 64];
     double x[kSumEach];
@@ -775,38 +787,36 @@ hipError_t launch_mx_reduce(const MxReduceArgs &args, int lds_per_cu, hipStream_
         return hipSuccess;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
     const unsigned lds = reserve(lds_per_cu, f.waves, unsigned(f.tiles * kTileElems * sizeof(uint16_t)));
-    switch (f.tiles) {
-    case 2: hipLaunchKernelGGL(mx_reduce_wide_kernel<2>, grid, block, lds, stream, a); break;
-    case 4: hipLaunchKernelGGL(mx_reduce_wide_kernel<4>, grid, block, lds, stream, a); break;
-    default: hipLaunchKernelGGL(mx_reduce_kernel, grid, block, 0, stream, a); break;
-    }
+    if (f.tiles == 1)
+        hipLaunchKernelGGL(mx_reduce_kernel, grid, block, 0, stream, a);
+    else if (a.in.n < kFew)
+        hipLaunchKernelGGL((mx_reduce_wide_kernel<4, kFew>), grid, block, lds, stream, a);
+    else if (f.tiles == 2)
+        hipLaunchKernelGGL((mx_reduce_wide_kernel<2, kBatch>), grid, block, lds, stream, a);
+    else
+        hipLaunchKernelGGL((mx_reduce_wide_kernel<4, kBatch>), grid, block, lds, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, int lds_per_cu, hipStream_t stream) {
+hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, hipStream_t stream) {
     MxNormArgs a = args;
     const ReduceForm f = reduce_form(a.in.n, a.walk.count);
     if (f.tiles > 1)
         a.walk = args.units;
     else
         a.walk.by_xcd = 1;
-    if (a.walk.count > 0) {
-        const dim3 grid(grid_for(a.walk.count)), block(kBlock);
-        const unsigned lds = reserve(lds_per_cu, f.waves, 0);
-        switch (f.tiles) {
-        case 2: hipLaunchKernelGGL(mx_norm_wide_kernel<2>, grid, block, lds, stream, a); break;
-        case 4: hipLaunchKernelGGL(mx_norm_wide_kernel<4>, grid, block, lds, stream, a); break;
-        default: hipLaunchKernelGGL(mx_norm_kernel, grid, block, 0, stream, a); break;
-        }
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-    }
-    if (a.walk.count <= kSumOnce) {
-        hipLaunchKernelGGL(mx_sum_kernel, dim3(1), dim3(kSumItems), 0, stream, a.partial, a.walk.count, norm_sq);
-        return hipGetLastError();
-    }
-    return launch_tile_sums(a.partial, a.walk.count, norm_sq, stream);
+    const dim3 grid(grid_for(a.walk.count < kMxNormWaves ? a.walk.count : kMxNormWaves)), block(kBlock);
+    if (f.tiles == 1)
+        hipLaunchKernelGGL(mx_norm_kernel, grid, block, 0, stream, a);
+    else if (a.in.n < kFew)
+        hipLaunchKernelGGL((mx_norm_wide_kernel<4, kFew>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx_norm_wide_kernel<2, kBatch>), grid, block, 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(mx_sum_kernel, dim3(1), dim3(kSumItems), 0, stream, a.partial, int64_t(grid.x), norm_sq);
+    return hipGetLastError();
 }
 
 // Waves that share a compute unit in the step. Long launches, Llama-3-8B
