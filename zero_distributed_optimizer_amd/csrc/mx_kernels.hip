@@ -384,10 +384,15 @@ __device__ __forceinline__ void norm_tile(const MxNormArgs &a, const MxTile &t, 
     const Slots own = slots_of(t.lo, t.own);
     s.add<8>(acc, a.scale, own.lo, own.hi);
 }
-__device__ __forceinline__ void put_partial(double *at, double s) {
+// A wave's lanes added by a fixed butterfly.
+__device__ __forceinline__ double lanes_total(double s) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         s = s + __shfl_xor(s, off, 64);
+    return s;
+}
+__device__ __forceinline__ void put_partial(double *at, double s) {
+    s = lanes_total(s);
     if (threadIdx.x == 0)
         *at = s;
 }
@@ -425,35 +430,51 @@ void mx_norm_wide_kernel(MxNormArgs a) {
     put_partial(a.partial + blockIdx.x, s.total());
 }
 
-// The waves' sums added by one workgroup: work-item t takes sums t, t + 1024,
-// ..., all loads first, then a fixed butterfly over each wave and the 16
-// waves' sums in order.
-constexpr int kSumItems = 1024, kSumEach = int(kMxNormWaves / kSumItems);
+// The sums of a workgroup's waves (threadIdx.y), added in order by its first
+// work-item.
+template <int kWaves>
+__device__ __forceinline__ void put_total(double s, double *out) {
+    __shared__ double waves[kWaves];
+    s = lanes_total(s);
+    if (threadIdx.x == 0)
+        waves[threadIdx.y] = s;
+    __syncthreads();
+    if (threadIdx.x == 0 && threadIdx.y == 0) {
+        double t = waves[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+            t = t + waves[w];
+        *out = t;
+    }
+}
+
+// The norms' wave sums added by one workgroup: work-item t takes sums t, t +
+// 1024, ..., all loads first.
+constexpr int kSumWaves = 16, kSumItems = 64 * kSumWaves, kSumEach = int(kMxNormWaves / kSumItems);
 __global__ __launch_bounds__(kSumItems) void mx_sum_kernel(const double *partial, int64_t n, double *out) {
-    __shared__ double waves[kSumItems / 64];
     double x[kSumEach];
 #pragma unroll
     for (int j = 0; j < kSumEach; ++j) {
-        const int64_t i = int64_t(j) * kSumItems + threadIdx.x;
+        const int64_t i = int64_t(j) * kSumItems + threadIdx.y * 64 + threadIdx.x;
         x[j] = i < n ? partial[i] : 0.0;
     }
     double s = x[0];
 #pragma unroll
     for (int j = 1; j < kSumEach; ++j)
         s = s + x[j];
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        s = s + __shfl_xor(s, off, 64);
-    if (threadIdx.x % 64 == 0)
-        waves[threadIdx.x / 64] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = waves[0];
-#pragma unroll
-        for (int w = 1; w < kSumItems / 64; ++w)
-            t = t + waves[w];
-        *out = t;
-    }
+    put_total<kSumWaves>(s, out);
+}
+
+// The norm of a few tiles in one launch instead of two: up to 64 tiles, and 512
+// tiles times contributions (8 contributions of 16 tiles 6.9 us a call, 10.2
+// in two launches, of 63 tiles both 10.1 but the step behind it 3 us sooner;
+// 64 contributions of 32 tiles 19.1 and 10.2).
+constexpr int64_t kNormAtOnceTiles = 64, kNormAtOnceWork = 512;
+__global__ __launch_bounds__(kSumItems) void mx_norm_at_once_kernel(MxNormArgs a, double *out) {
+    Squares s;
+    for (int64_t i = threadIdx.y; i < a.walk.count; i += kSumWaves)
+        norm_tile(a, local_tile(a.walk, i), s);
+    put_total<kSumWaves>(s.total(), out);
 }
 
 // ---- the step --------------------------------------------------------------------------------
@@ -800,6 +821,10 @@ hipError_t launch_mx_reduce(const MxReduceArgs &args, int lds_per_cu, hipStream_
 
 hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, hipStream_t stream) {
     MxNormArgs a = args;
+    if (a.walk.count <= kNormAtOnceTiles && a.walk.count * a.in.n <= kNormAtOnceWork) {
+        hipLaunchKernelGGL(mx_norm_at_once_kernel, dim3(1), dim3(64, kSumWaves), 0, stream, a, norm_sq);
+        return hipGetLastError();
+    }
     const ReduceForm f = reduce_form(a.in.n, a.walk.count);
     if (f.tiles > 1)
         a.walk = args.units;
@@ -815,7 +840,7 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, hipStream_t s
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(mx_sum_kernel, dim3(1), dim3(kSumItems), 0, stream, a.partial, int64_t(grid.x), norm_sq);
+    hipLaunchKernelGGL(mx_sum_kernel, dim3(1), dim3(64, kSumWaves), 0, stream, a.partial, int64_t(grid.x), norm_sq);
     return hipGetLastError();
 }
 
