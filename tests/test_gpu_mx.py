@@ -301,6 +301,23 @@ def test_long_reductions(gpu, n):
     free()
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 64])
+@pytest.mark.parametrize("size", [1, 3000, 32_000, 40_000, 300_000])
+def test_norm_of_few_and_many_tiles(either, size, n):
+    """On both sides of the lengths at which the norm's form changes; the
+    squares of a rank's ranges beside padding and cut tiles."""
+    gpu, rng = either, np.random.default_rng(size + n)
+    lay = OL.build_layout([size, 77], size, 2)
+    for r in range(2):
+        plan = gpu.build_range_map([size, 77], size, 2, r)
+        store = random_mx(rng, lay, gpu.LOCAL)
+        dev = dev_mx(store)
+        ws = torch.full((max(16, plan.norm_mxfp4_workspace_bytes),), FILL, dtype=torch.uint8, device=DEV)
+        ns = torch.full((1,), -1.0, dtype=torch.float64, device=DEV)
+        gpu.grad_norm_sq_mxfp4(plan, [dev] * n, gpu.LOCAL, 0.3, ws, ns)
+        assert_norm(float(ns), MX.norm_sq(lay, r, [store] * n, gpu.LOCAL, 0.3), plan.owned_numel, f"r={r}")
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_norm(either, seed):
     gpu = either
