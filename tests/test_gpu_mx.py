@@ -437,14 +437,17 @@ def test_rank_with_only_padding(gpu):
 
 def test_per_bucket_calls_equal_the_whole(gpu):
     pr, sizes, bucket, D = layout_of(41, dps=(4,))
-    sizes, bucket = sizes + [9000, 77, 5000], 4000
+    sizes, bucket = sizes + [9000, 77, 5000, 1400, 1500, 1600, 2000, 3000], 1500
     lay = OL.build_layout(sizes, bucket, D)
     rng = np.random.default_rng(1)
     plan = gpu.build_range_map(sizes, bucket, D, 2)
     stores, dev = sources(gpu, rng, lay, 2, D, gpu.WORLD)
     st0 = state_of(rng, plan.shard_numel)
     res = []
-    for parts in ([None], [(b, b + 1) for b in reversed(range(len(lay.buckets)))]):
+    nb = len(lay.buckets)
+    assert nb >= 4
+    for parts in ([None], [(b, b + 1) for b in reversed(range(nb))],
+                  [[(b, b + 1) for b in range(k, nb, 3)] for k in (1, 0, 2)] + [[], [(2, 2)]]):
         st, mx = [to_dev(x) for x in st0], gpu.mx_empty(plan, gpu.LOCAL)
         for b in parts:
             gpu.sharded_adam_step_mxfp4(plan, dev, gpu.WORLD, 0.25, *st, param_mx=mx, buckets=b,
@@ -454,8 +457,8 @@ def test_per_bucket_calls_equal_the_whole(gpu):
         gpu.writeback_params_mxfp4(plan, st[0], wb, gpu.LOCAL)
         assert torch.equal(wb[0], mx[0]) and torch.equal(wb[1], mx[1])
         res.append(st + list(mx))
-    for a, b in zip(*res):
-        assert torch.equal(a, b)
+    for other in res[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(res[0], other))
     free()
 
 
@@ -721,6 +724,38 @@ def test_calls_on_another_stream(gpu):
         assert torch.equal(d, ref["out"])
     for x, y in zip(a["st"] + b["st"], ref["st"] * 2):
         assert all(torch.equal(p, q) for p, q in zip(x, y))
+    free()
+
+
+def test_two_threads(gpu):
+    """Two host threads, each with a stream and buffers of its own, on one set
+    of plans."""
+    import threading
+    loop = Loop(gpu, [50000, 17, 20000], 30000, 4)
+    ref, sets, errors = loop.device(), [loop.device() for _ in range(2)], []
+    for t in range(1, 9):
+        loop.run(ref, t, 0.05)
+    torch.cuda.synchronize()
+
+    def work(d):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for t in range(1, 9):
+                    loop.run(d, t, 0.05)
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for d in sets:
+        assert torch.equal(d["out"], ref["out"])
+        for x, y in zip(d["st"], ref["st"]):
+            assert all(torch.equal(p, q) for p, q in zip(x, y))
     free()
 
 

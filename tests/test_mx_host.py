@@ -88,6 +88,19 @@ def test_binding_refuses_before_the_library():
     assert not c.any() and not s.any()
 
 
+def test_bucket_lists():
+    plan = Z.build_range_map([10] * 9, 10, 2, 0)
+    assert plan.num_buckets == 9
+    ranges = ZM._Call(plan).buckets
+    assert list(ranges(None)) == [(0, 9)] and list(ranges((2, 5))) == [(2, 5)] and list(ranges((9, 9))) == [(9, 9)]
+    assert list(ranges([(5, 7), (0, 2), (2, 3), (4, 4)])) == [(0, 3), (5, 7)]
+    assert list(ranges([])) == [] and list(ranges([(3, 3)])) == []
+    for bad in ([(0, 2), (1, 3)], [(0, 2), (0, 2)], [(-1, 2)], [(3, 2)], [(0, 10)]):
+        with pytest.raises(Z.ZdoError) as e:
+            ranges(bad)
+        assert e.value.code == Z.EINVAL
+
+
 def test_calls_on_a_host_only_plan_are_errors():
     import ctypes
 

@@ -19,7 +19,8 @@ import ctypes
 
 import numpy as np
 
-from . import LOCAL, WORLD, Adam, Plan, _check, _dev_ptr, _stream, _torch, adam_hparams, require_library
+from . import (EINVAL, LOCAL, WORLD, Adam, Plan, ZdoError, _bucket_list, _check, _dev_ptr, _stream, _torch,
+               adam_hparams, require_library)
 
 MX_BUCKET_DTYPE = np.dtype([("block0", "<i8"), ("blocks", "<i8")])
 BLOCK = 32                # elements that share a scale
@@ -140,35 +141,54 @@ class _Call:
         return _stream(stream, self.device)
 
     def buckets(self, buckets):
+        """The bucket ranges to launch: all buckets, one (begin, end), or a list
+        of disjoint pairs, sorted and merged where they touch."""
         if buckets is None:
-            return 0, self.plan.num_buckets
-        return int(buckets[0]), int(buckets[1])
+            return ((0, self.plan.num_buckets),)
+        if _bucket_list(buckets) is None:
+            return ((int(buckets[0]), int(buckets[1])),)
+        runs = []
+        for b, e in sorted((int(b), int(e)) for b, e in buckets):
+            if not 0 <= b <= e <= self.plan.num_buckets:
+                raise ZdoError(EINVAL, f"bucket range ({b}, {e}): need 0 <= begin <= end <= {self.plan.num_buckets}")
+            if b == e:
+                continue
+            if runs and b < runs[-1][1]:
+                raise ZdoError(EINVAL, f"bucket ranges {runs[-1]} and ({b}, {e}) overlap")
+            if runs and b == runs[-1][1]:
+                runs[-1] = (runs[-1][0], e)
+            else:
+                runs.append((b, e))
+        return runs
 
 
 def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buckets=None, stream=None) -> None:
     """The bf16 gradient buffer to MXFP4, into the storage `out` (both in
     `coords`). residual: a float32 tensor as long as grads, added first and
-    left holding what the 4 bits did not carry. buckets=(begin, end): those
-    buckets only."""
+    left holding what the 4 bits did not carry. buckets=(begin, end), or a
+    list of disjoint such pairs: those buckets only, one launch for each run
+    of them that touch."""
     call, n = _Call(plan), plan.extent(coords)
     g = call.ptr(grads, "grads", "bf16", n)
     r = call.opt(residual, "residual", "f32", n)
     c, s = call.storage(out, "out", coords)
-    b0, b1 = call.buckets(buckets)
-    _check(require_library().quantize_grads_mxfp4(plan.handle, b0, b1, g, coords, r, c, s, call.stream(stream)))
+    st, L = call.stream(stream), require_library()
+    for b0, b1 in call.buckets(buckets):
+        _check(L.quantize_grads_mxfp4(plan.handle, b0, b1, g, coords, r, c, s, st))
 
 
 def reduce_scatter_local_mxfp4(plan: Plan, contributions, coords: int, scale: float, out, out_coords: int,
                                stream=None, buckets=None) -> None:
     """reduce_scatter_local of contributions in MXFP4 (storages in `coords`):
     bf16(scale * sum) over the rank's ranges. One contribution and scale 1
-    give its values. buckets=(begin, end): those buckets only."""
+    give its values. buckets: as quantize_grads_mxfp4."""
     call = _Call(plan)
     mx = call.inputs(contributions, "contributions", coords)
     o = call.ptr(out, "out", "bf16", plan.extent(out_coords))
-    b0, b1 = call.buckets(buckets)
-    _check(require_library().reduce_scatter_local_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords,
-                                                        scale, o, out_coords, call.stream(stream)))
+    st, L = call.stream(stream), require_library()
+    for b0, b1 in call.buckets(buckets):
+        _check(L.reduce_scatter_local_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, o,
+                                            out_coords, st))
 
 
 def grad_norm_sq_mxfp4(plan: Plan, contributions, coords: int, scale: float, workspace, norm_sq_out,
@@ -192,8 +212,8 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     """sharded_adam_step on contributions in MXFP4 (storages in `coords`). The
     updated parameters go to param_out (bf16) and, rounded to MXFP4, to the
     storage param_mx. grad_coeff: a one-element float32 device tensor that
-    multiplies the main grad (NaN skips the step). buckets=(begin, end):
-    those buckets only."""
+    multiplies the main grad (NaN skips the step). buckets: as
+    quantize_grads_mxfp4."""
     call, L = _Call(plan), plan.shard_numel
     mx = call.inputs(contributions, "contributions", coords)
     m = call.ptr(master, "master", "f32", L)
@@ -204,10 +224,10 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     gc = call.opt(grad_coeff, "grad_coeff", "f32", 1)
     mg = call.opt(main_grad_out, "main_grad_out", "f32", L)
     hp = adam_hparams(lr, beta1, beta2, eps, weight_decay, step)
-    b0, b1 = call.buckets(buckets)
-    _check(require_library().sharded_adam_step_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale,
-                                                     m, a, v, p, param_coords, pc, ps, param_mx_coords,
-                                                     ctypes.byref(hp), gc, mg, call.stream(stream)))
+    st, L = call.stream(stream), require_library()
+    for b0, b1 in call.buckets(buckets):
+        _check(L.sharded_adam_step_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, m, a, v, p,
+                                         param_coords, pc, ps, param_mx_coords, ctypes.byref(hp), gc, mg, st))
 
 
 def writeback_params_mxfp4(plan: Plan, master, out, coords: int, stream=None) -> None:
