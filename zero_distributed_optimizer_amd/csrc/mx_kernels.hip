@@ -607,10 +607,15 @@ __device__ __forceinline__ void step_edge(const MxStepArgs &a, const MxTile &t, 
     }
 }
 
-// The occupancy bounds let the compiler keep every load of a batch in
-// flight; the launches cap the waves anyway.
-template <int kN>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 4))) void mx_step_kernel(MxStepArgs a) {
+// The occupancy bound tells the compiler how many registers a wave may have,
+// and so how many of a tile's loads it puts in flight before the first wait:
+// 4 waves a SIMD serve long launches of 8 and 16 contributions best (4778 and
+// 2842 us; 4812 and 2926 with 5), 5 the short ones (GPT-2 small rank 78.9 us,
+// 80.6 with 4, 82.9 with 6; fragmented 32.7, 34.1, 32.7) and other counts (3
+// contributions of 3e8 1376 us, 1396 with 4; 12 of 1.5e8 790 and 799).
+template <int kN, bool kShort>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, kN > 0 && !kShort ? 4 : 5)))
+void mx_step_kernel(MxStepArgs a) {
     __shared__ f32x4 sums[kTileElems / 4];
     const bool clip = a.coeff != nullptr;
     const float cf = clip ? *ro(a.coeff) : 1.0f;
@@ -861,19 +866,22 @@ hipError_t launch_mx_step(const MxStepArgs &args, int lds_per_cu, hipStream_t st
     if (args.walk.count <= 0)
         return hipSuccess;
     MxStepArgs a = args;
-    a.walk.by_xcd = a.walk.count < kShortLaunch || a.in.n >= 8;
+    const bool is_short = a.walk.count < kShortLaunch;
+    a.walk.by_xcd = is_short || a.in.n >= 8;
     const dim3 grid(grid_for(a.walk.count)), block(kBlock);
     const bool fixed = a.in.n == 8 || a.in.n == 16;
-    const unsigned lds = reserve(lds_per_cu,
-                                 a.walk.count < kShortLaunch ? kStepWavesShort
-                                 : fixed                     ? kStepWavesFixed
-                                                             : kStepWaves,
+    const unsigned lds = reserve(lds_per_cu, is_short ? kStepWavesShort : fixed ? kStepWavesFixed : kStepWaves,
                                  kTileElems * sizeof(float));
-    switch (a.in.n) {
-    case 8: hipLaunchKernelGGL(mx_step_kernel<8>, grid, block, lds, stream, a); break;
-    case 16: hipLaunchKernelGGL(mx_step_kernel<16>, grid, block, lds, stream, a); break;
-    default: hipLaunchKernelGGL(mx_step_kernel<0>, grid, block, lds, stream, a); break;
-    }
+    if (a.in.n == 8 && is_short)
+        hipLaunchKernelGGL((mx_step_kernel<8, true>), grid, block, lds, stream, a);
+    else if (a.in.n == 8)
+        hipLaunchKernelGGL((mx_step_kernel<8, false>), grid, block, lds, stream, a);
+    else if (a.in.n == 16 && is_short)
+        hipLaunchKernelGGL((mx_step_kernel<16, true>), grid, block, lds, stream, a);
+    else if (a.in.n == 16)
+        hipLaunchKernelGGL((mx_step_kernel<16, false>), grid, block, lds, stream, a);
+    else
+        hipLaunchKernelGGL((mx_step_kernel<0, true>), grid, block, lds, stream, a);
     return hipGetLastError();
 }
 
