@@ -840,7 +840,7 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, hipStream_t s
         hipLaunchKernelGGL(mx_norm_kernel, grid, block, 0, stream, a);
     else if (a.in.n < kFew)
         hipLaunchKernelGGL((mx_norm_wide_kernel<4, kFew>), grid, block, 0, stream, a);
-    else   // 2 tiles at a time, 4 within 2% of it from 5 to 64 contributions
+    else
         hipLaunchKernelGGL((mx_norm_wide_kernel<2, kBatch>), grid, block, 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
