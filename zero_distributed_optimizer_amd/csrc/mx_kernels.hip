@@ -409,6 +409,9 @@ __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
         norm_tile(a, local_tile(a.walk, launch_order(a.walk.by_xcd, a.walk.count, i)), s);
     put_partial(a.partial + blockIdx.x, s.total());
 }
+// From kFew contributions by 2 tiles (4: 4 contributions of 1e8 slots 49.0 us
+// instead of 50.2, 8 of 1e8 76.0 and 75.7, 12 of 8e7 90.9 and 88.0, 16 of 6e7
+// 87.2 and 85.8, 32 of 4e7 113.6 and 110.9, 64 of 3e7 168.9 and 168.1).
 template <int kW, int kMost>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, kMost < kBatch ? 8 : 4)))
 void mx_norm_wide_kernel(MxNormArgs a) {
