@@ -398,6 +398,142 @@ def test_step_random_layouts(gpu, seed):
     free()
 
 
+@pytest.fixture()
+def long_forms(gpu):
+    """The build that takes the forms for long launches at any length."""
+    with Z.use_library(ZB.GRID_LOOP_LIB):
+        yield gpu
+        free()
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_step_random_layouts_in_the_long_forms(long_forms, seed):
+    """Random layouts through the step's kernels for long launches: 8 and 16
+    contributions have kernels of their own there, other counts one."""
+    gpu = long_forms
+    pr, sizes, bucket, D = layout_of(1100 + seed)
+    sizes = sizes + [pr.randint(3000, 9000)]   # whole tiles in some range
+    rng = np.random.default_rng(seed)
+    lay = OL.build_layout(sizes, bucket, D)
+    nb = len(lay.buckets)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=pr.choice([0.999, 0.95]), eps=1e-8, weight_decay=pr.choice([0.0, 0.1]))
+    n = (8, 16, 8, 16, pr.randint(1, 64))[seed % 5]
+    for r in sorted({0, D - 1, pr.randrange(D)}):
+        coords = pr.choice([gpu.WORLD, gpu.LOCAL])
+        stores, dev = sources(gpu, rng, lay, r, n, coords, lo=100, hi=140)
+        b0 = pr.randrange(nb)
+        check_step(gpu, sizes, bucket, D, r, stores, dev, coords, pr.choice([1.0 / n, 0.3]), hp, pr.choice([1, 7, 900]),
+                   state_of(rng, OL.shard_numel(lay, r)), pc=pr.choice([None, gpu.WORLD, gpu.LOCAL]),
+                   mc=pr.choice([None, gpu.WORLD, gpu.LOCAL]), coeff=pr.choice([None, 0.37, 1.0]), mg=pr.random() < 0.5,
+                   buckets=pr.choice([None, (b0, pr.randint(b0, nb))]))
+
+
+@pytest.mark.parametrize("n", [2, 8, 16])
+def test_step_specials_in_the_long_forms(long_forms, n):
+    """Any scale byte, 255 among them, and a NaN coefficient, which skips the step."""
+    gpu = long_forms
+    sizes, bucket, D = [6000, 9], 7000, 2
+    lay = OL.build_layout(sizes, bucket, D)
+    rng = np.random.default_rng(n)
+    hp = W.get("tiny").hp
+    stores = [random_mx(rng, lay, gpu.LOCAL, 0, 256) for _ in range(n)]
+    dev = [dev_mx(s) for s in stores]
+    for r in range(D):
+        st = state_of(rng, OL.shard_numel(lay, r))
+        k = OL.shard_bases(lay, r)[0][0]
+        st[0][k + 700], st[0][k + 1400] = np.inf, np.nan
+        check_step(gpu, sizes, bucket, D, r, stores, dev, gpu.LOCAL, 0.5, hp, 2, st, pc=gpu.WORLD, mc=gpu.WORLD, mg=True)
+        got, _ = check_step(gpu, sizes, bucket, D, r, stores, dev, gpu.LOCAL, 0.5, hp, 2, st, pc=gpu.LOCAL,
+                            mc=gpu.LOCAL, coeff=float("nan"), mg=True)
+        for a, b in zip(got, st):
+            assert np.array_equal(host_f32(a).view(np.uint32), b.view(np.uint32))
+
+
+def test_long_steps(gpu):
+    """35 M slots in ragged buckets, above the length from which the library
+    itself takes the step's forms for long launches; every slot compared."""
+    sizes, bucket, D = [9_000_001, 65, 8_999_999, 33, 17_000_011], 10_000_000, 1
+    lay = OL.build_layout(sizes, bucket, D)
+    plan = gpu.build_range_map(sizes, bucket, D, 0)
+    assert plan.mx_blocks(gpu.LOCAL) // 16 > 1 << 16
+    rng, hp, Ln = np.random.default_rng(9), W.get("gpt2_small").hp, plan.shard_numel
+    host = [random_mx(rng, lay, gpu.LOCAL, lo=108, hi=124) for _ in range(3)]
+    dev = [dev_mx(s) for s in host]
+    state = state_of(rng, Ln)
+    ranges = MX.ranges(lay, 0)
+    values = [[MX._values(s, MX.LOCAL, x)[:x[1] - x[0].start].astype(np.float32) for s in host] for x in ranges]
+    for n in (3, 8, 16):
+        order = [(j * j + j // 3) % 3 for j in range(n)]
+        st = [to_dev(x) for x in state]
+        par = torch.full((Ln,), SENTINEL, dtype=torch.int16, device=DEV)
+        mx = dev_mx(MX.empty(lay, MX.LOCAL, FILL))
+        gpu.sharded_adam_step_mxfp4(plan, [dev[j] for j in order], gpu.LOCAL, 0.3, *st, par, gpu.LOCAL, param_mx=mx,
+                                    **hp_kwargs(hp, 5))
+        got, got_par, got_mx = [host_f32(x) for x in st], host_u16(par), host_mx(mx)
+        want_mx, rest = MX.empty(lay, MX.LOCAL, FILL), np.ones(Ln, bool)
+        for b, (x, v) in enumerate(zip(ranges, values)):
+            acc = v[order[0]]
+            for j in order[1:]:
+                acc = acc + v[j]
+            k = slice(x[2], x[2] + acc.size)
+            want = MX.adam(ON.hp_array(hp, 5), acc * np.float32(0.3), *(s[k] for s in state), np.float32)
+            for g, w, name in zip(got, want, ("master", "exp_avg", "exp_avg_sq")):
+                assert_f32(g[k], w, f"n={n} bucket {b} {name}")
+            assert_bf16(got_par[k], ON.narrow(want[0]), f"n={n} bucket {b} parameters")
+            MX._put(want_mx, MX.LOCAL, x, want[0])
+            rest[k] = False
+        assert_mx(mx, want_mx, f"n={n} MXFP4 parameters")
+        assert (got_par[rest] == SENTINEL).all()
+        for g, s in zip(got, state):
+            assert np.array_equal(g[rest].view(np.uint32), s[rest].view(np.uint32))
+    free()
+
+
+def test_step_beyond_32_bits(gpu):
+    """8 contributions to 1.1e9 slots (state offsets past 2^32 bytes), the
+    last two of three buckets: their heads, middles and tails against the
+    oracle, the first bucket as it was."""
+    sizes, bucket, D, n = [400_000_007, 400_000_065, 300_004_099], 400_000_000, 1, 8
+    lay = OL.build_layout(sizes, bucket, D)
+    plan = gpu.build_range_map(sizes, bucket, D, 0)
+    Ln, hp = plan.shard_numel, W.get("llama3_8b").hp
+    assert 4 * Ln > 1 << 32 and len(lay.buckets) == 3
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    blocks = plan.mx_blocks(gpu.LOCAL)
+    dev = [(torch.randint(0, 256, (blocks, 16), dtype=torch.uint8, device=DEV, generator=gen),
+            torch.randint(108, 124, (blocks,), dtype=torch.uint8, device=DEV, generator=gen)) for _ in range(3)]
+    order = [(j * j + j // 3) % 3 for j in range(n)]
+    st = [torch.randn(Ln, device=DEV, generator=gen) * 0.02, torch.randn(Ln, device=DEV, generator=gen) * 1e-3]
+    st.append((torch.randn(Ln, device=DEV, generator=gen) * 1e-3).square_())
+    before = [x.clone() for x in st]
+    par = torch.full((Ln,), SENTINEL, dtype=torch.int16, device=DEV)
+    gpu.sharded_adam_step_mxfp4(plan, [dev[j] for j in order], gpu.LOCAL, 0.25, *st, par, gpu.LOCAL, buckets=(1, 3),
+                                **hp_kwargs(hp, 5))
+    ranges = MX.ranges(lay, 0)
+    head = ranges[1][2]
+    for a, b in zip(st, before):
+        assert torch.equal(a[:head], b[:head])
+    assert bool((par[:head] == SENTINEL).all())
+    for x in ranges[1:]:
+        size, phase, blk = x[1] - x[0].start, x[3], x[5]
+        for lo in (0, size // 2, size - 5000):
+            # the blocks over elements [lo, lo + 5000) of the bucket
+            b0, b1 = (phase + lo) // 32, (phase + lo + 5000 + 31) // 32
+            at = slice(phase + lo - 32 * b0, phase + lo - 32 * b0 + 5000)
+            part = slice(blk.start + b0, blk.start + b1)
+            v = [MX.decode(c[part].cpu().numpy(), s[part].cpu().numpy()).reshape(-1)[at].astype(np.float32)
+                 for c, s in dev]
+            acc = v[order[0]]
+            for j in order[1:]:
+                acc = acc + v[j]
+            k = slice(x[2] + lo, x[2] + lo + 5000)
+            want = MX.adam(ON.hp_array(hp, 5), acc * np.float32(0.25), *(host_f32(s[k]) for s in before), np.float32)
+            for g, w, name in zip(st, want, ("master", "exp_avg", "exp_avg_sq")):
+                assert_f32(host_f32(g[k]), w, f"{name} from {lo}")
+            assert_bf16(host_u16(par[k]), ON.narrow(want[0]), f"parameters from {lo}")
+    free()
+
+
 def test_step_specials(gpu):
     """Scale 255, sums that overflow, subnormal values, a NaN coefficient that
     skips the step, an Inf master in the MXFP4 output."""

@@ -16,6 +16,7 @@ import oracle.layout as OL
 import oracle.mx as MX
 import workloads as W
 import zero_distributed_optimizer_amd as Z
+from zero_distributed_optimizer_amd import build as ZB
 from zero_distributed_optimizer_amd import mx as ZM
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -120,3 +121,14 @@ def test_calls_on_a_host_only_plan_are_errors():
     assert L.writeback_params_mxfp4(h, 16, 32, 48, 0, None) == Z.EHIP
     assert L.all_gather_params_mxfp4(h, two, two, 2, 0, 16, None) == Z.EHIP
     assert b"device" in L.zdo_last_error()
+
+
+def test_the_test_build_reaches_every_form_for_long_launches():
+    """Each launch length at which the MXFP4 kernels change their form is a
+    macro, and the test build sets it to one tile."""
+    text = open(os.path.join(CSRC, "mx_kernels.hip")).read()
+    lengths = set(re.findall(r"#ifndef (ZDO_MX_\w+_TILES)", text))
+    assert re.search(r"constexpr int64_t kShortLaunch = ZDO_MX_LONG_TILES;", text)
+    assert lengths == {"ZDO_MX_WIDE_TILES", "ZDO_MX_LONG_TILES"}
+    for name in lengths:
+        assert f"-D{name}=1" in ZB.GRID_LOOP_FLAGS

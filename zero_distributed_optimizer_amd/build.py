@@ -21,9 +21,9 @@ LIB = os.path.join(HERE, "libzdo.so")
 # A test build whose launches are capped at 64 workgroups, so that every
 # kernel walks its tiles through the grid-stride continuation (in the real
 # build only launches of more than 2^24 tiles do), and whose MXFP4 reductions
-# take their forms for long launches at any length.
+# and steps take their forms for long launches at any length.
 GRID_LOOP_LIB = os.path.join(HERE, "libzdo_gridloop.so")
-GRID_LOOP_FLAGS = ["-DZDO_MAX_GRID=64", "-DZDO_MX_WIDE_TILES=1"]
+GRID_LOOP_FLAGS = ["-DZDO_MAX_GRID=64", "-DZDO_MX_WIDE_TILES=1", "-DZDO_MX_LONG_TILES=1"]
 SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "mx_abi.cpp", "mx_kernels.hip"]
 HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h"]
 

@@ -87,7 +87,10 @@ __device__ __forceinline__ MxTile local_tile(const MxWalk &wk, int64_t i) {
 // Launches of fewer tiles than kShortLaunch are short. The step at 4e7 slots:
 // 8 contributions 197 us as a long launch, 201 as a short one, 3 contributions
 // 189 and 193; at 2e7 slots 101.6 and 102.7, 99.3 and 96.5.
-constexpr int64_t kShortLaunch = int64_t(1) << 16;
+#ifndef ZDO_MX_LONG_TILES
+#define ZDO_MX_LONG_TILES (int64_t(1) << 16)
+#endif
+constexpr int64_t kShortLaunch = ZDO_MX_LONG_TILES;
 __device__ __forceinline__ int64_t launch_order(bool by_xcd, int64_t count, int64_t i) {
     if (!by_xcd || i >= count / 64 * 64)
         return i;
