@@ -398,6 +398,50 @@ def test_step_random_layouts(gpu, seed):
     free()
 
 
+@pytest.mark.parametrize("n", [*range(1, 20), 24, 31, 32, 33, 48, 63, 64])
+def test_step_every_small_count(either, n):
+    """Every number of contributions around the kernels' fixed counts and
+    batches, over ranges of whole tiles beside their cut ends, at scales far
+    enough apart that the order of the sum shows; every place of the
+    parameters, with and without a coefficient and the main grad."""
+    gpu = either
+    sizes, bucket, D, r = [9000, 33, 2049], 7000, 2, 1
+    lay = OL.build_layout(sizes, bucket, D)
+    rng = np.random.default_rng(n)
+    st = state_of(rng, OL.shard_numel(lay, r))
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+    stores = {c: sources(gpu, rng, lay, r, n, c, lo=100, hi=140) for c in (gpu.WORLD, gpu.LOCAL)}
+    k = 0
+    for pc in (None, gpu.WORLD, gpu.LOCAL):
+        for mc in (None, gpu.WORLD, gpu.LOCAL):
+            for coeff in (None, 0.37):
+                k += 1
+                coords = (gpu.WORLD, gpu.LOCAL)[k % 2]
+                check_step(gpu, sizes, bucket, D, r, *stores[coords], coords, 1.0 / n, hp, 5, st, pc=pc, mc=mc,
+                           coeff=coeff, mg=k % 3 == 0)
+
+
+def test_the_order_of_the_sum_shows():
+    """The contributions of the test above, summed in any other order, or in
+    parts, differ from the stated order."""
+    lay = OL.build_layout([9000, 33, 2049], 7000, 2)
+    for n in (7, 8, 9, 15, 16, 17):
+        rng = np.random.default_rng(n)
+        stores = [random_mx(rng, lay, MX.LOCAL, lo=100, hi=140) for _ in range(n)]
+        v = [MX._values(s, MX.LOCAL, MX.ranges(lay, 1)[0]).astype(np.float32) for s in stores]
+
+        def total(x):
+            acc = x[0]
+            for y in x[1:]:
+                acc = acc + y
+            return acc
+        want = total(v)
+        swapped = v[:n // 2 - 1] + [v[n // 2], v[n // 2 - 1]] + v[n // 2 + 1:]
+        for other in (total(v[::-1]), total(swapped), total(v[:n // 2]) + total(v[n // 2:]),
+                      total([total(v[0::2]), total(v[1::2])]), total(v[:-1])):
+            assert (other != want).any()
+
+
 @pytest.fixture()
 def long_forms(gpu):
     """The build that takes the forms for long launches at any length."""
