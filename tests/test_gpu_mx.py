@@ -318,6 +318,58 @@ def test_norm_of_few_and_many_tiles(either, size, n):
         assert_norm(float(ns), MX.norm_sq(lay, r, [store] * n, gpu.LOCAL, 0.3), plan.owned_numel, f"r={r}")
 
 
+@pytest.mark.parametrize("n, tiles", [(1, 63), (1, 64), (1, 65), (8, 63), (8, 64), (8, 65), (9, 56), (9, 57),
+                                      (64, 8), (64, 9)])
+def test_norm_at_the_change_of_its_form(either, n, tiles):
+    """One launch up to 64 tiles and 512 tiles times contributions, two above."""
+    gpu, rng = either, np.random.default_rng(64 * n + tiles)
+    size = 512 * tiles - 100
+    lay = OL.build_layout([size], size, 1)
+    plan = gpu.build_range_map([size], size, 1, 0)
+    assert plan.mx_blocks(gpu.LOCAL) == 16 * tiles
+    store = [random_mx(rng, lay, gpu.LOCAL) for _ in range(2)]
+    dev, order = [dev_mx(s) for s in store], [j % 2 for j in range(n)]
+    ws = torch.full((max(16, plan.norm_mxfp4_workspace_bytes),), FILL, dtype=torch.uint8, device=DEV)
+    ns = torch.full((1,), -1.0, dtype=torch.float64, device=DEV)
+    gpu.grad_norm_sq_mxfp4(plan, [dev[j] for j in order], gpu.LOCAL, 0.3, ws, ns)
+    assert_norm(float(ns), MX.norm_sq(lay, 0, [store[j] for j in order], gpu.LOCAL, 0.3), size, f"{tiles} tiles")
+
+
+@pytest.mark.parametrize("n, size", [(1, 10_000_003), (5, 8_388_609), (1, 35_000_003), (8, 34_000_001)])
+def test_norm_of_more_tiles_than_waves(gpu, n, size):
+    """A tile a wave beyond 16384 tiles, and units beyond 16384 of them: waves
+    that take several, every one of whose sums is added, in a workspace of
+    the stated size and nothing behind it."""
+    plan = gpu.build_range_map([size], size, 1, 0)
+    assert plan.norm_mxfp4_workspace_bytes == 8 * 16384
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    blocks = plan.mx_blocks(gpu.LOCAL)
+    two = [(torch.randint(0, 256, (blocks, 16), dtype=torch.uint8, device=DEV, generator=gen),
+            torch.randint(112, 128, (blocks,), dtype=torch.uint8, device=DEV, generator=gen)) for _ in range(2)]
+    order = [j % 2 for j in range(n)]
+    buf = torch.full((8 * 16384 + 4096,), FILL, dtype=torch.uint8, device=DEV)
+    ns = torch.full((1,), -1.0, dtype=torch.float64, device=DEV)
+    for _ in range(2):
+        gpu.grad_norm_sq_mxfp4(plan, [two[j] for j in order], gpu.LOCAL, 0.3, buf[:8 * 16384], ns)
+        assert bool((buf[8 * 16384:] == FILL).all())
+    v = [MX.decode(*host_mx(s)).reshape(-1)[:size].astype(np.float32) for s in two]
+    acc = v[order[0]]
+    for j in order[1:]:
+        acc = acc + v[j]
+    own = (acc * np.float32(0.3)).astype(np.float64)
+    assert_norm(float(ns), float(np.sum(own * own)), size, f"n={n}")
+    # the last slot alone, and one behind it that is no parameter element
+    for c, s in two:
+        s.fill_(0)
+        c.fill_(0)
+    at = (size - 1) // 32
+    two[0][0][at, (size - 1) % 32 // 2] = 0x77
+    two[0][1][at] = 127
+    gpu.grad_norm_sq_mxfp4(plan, [two[j] for j in order], gpu.LOCAL, 1.0, buf[:8 * 16384], ns)
+    assert size % 2 == 1 and float(ns) == (6.0 * order.count(0)) ** 2
+    free()
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_norm(either, seed):
     gpu = either
