@@ -1100,3 +1100,34 @@ def test_refusals(gpu):
             call()
         assert e.value.code == code
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("buckets", [[], [(1, 1)], (1, 1)])
+def test_refusals_without_buckets(gpu, buckets):
+    """Arguments are checked also where no bucket is asked for, as the bf16
+    calls do; a right call then changes nothing."""
+    plan = gpu.build_range_map([1000, 28], 600, 2, 1)
+    g = torch.full((plan.buffer_numel,), SENTINEL, dtype=torch.int16, device=DEV)
+    f = [torch.full((plan.shard_numel,), 1.5, device=DEV) for _ in range(3)]
+    hp = hp_kwargs(W.get("tiny").hp, 1)
+    local = gpu.mx_empty(plan, gpu.LOCAL)
+    for step, given, coords in ((gpu.sharded_adam_step_mxfp4, local, gpu.LOCAL), (gpu.sharded_adam_step, g, gpu.WORLD)):
+        for bad, code in ((dict(hp, step=0), gpu.EINVAL), (dict(hp, beta1=1.0), gpu.EINVAL)):
+            with pytest.raises(gpu.ZdoError) as e:
+                step(plan, [given], coords, 1.0, *f, buckets=buckets, **bad)
+            assert e.value.code == code
+        with pytest.raises(gpu.ZdoError) as e:
+            step(plan, [given], coords, 1.0, f[0], f[0], f[2], buckets=buckets, **hp)
+        assert e.value.code == gpu.EALIAS
+        with pytest.raises(gpu.ZdoError) as e:
+            step(plan, [given] * 65, coords, 1.0, *f, buckets=buckets, **hp)
+        assert e.value.code == gpu.EINVAL
+    with pytest.raises(gpu.ZdoError) as e:
+        gpu.reduce_scatter_local_mxfp4(plan, [], gpu.LOCAL, 1.0, g, gpu.WORLD, buckets=buckets)
+    assert e.value.code == gpu.EINVAL
+    world = gpu.mx_empty(plan, gpu.WORLD)
+    gpu.quantize_grads_mxfp4(plan, g, gpu.WORLD, world, buckets=buckets)
+    gpu.reduce_scatter_local_mxfp4(plan, [local], gpu.LOCAL, 1.0, g, gpu.WORLD, buckets=buckets)
+    gpu.sharded_adam_step_mxfp4(plan, [local], gpu.LOCAL, 1.0, *f, g, gpu.WORLD, buckets=buckets, **hp)
+    torch.cuda.synchronize()
+    assert bool((g == SENTINEL).all()) and not world[0].any() and all(bool((x == 1.5).all()) for x in f)

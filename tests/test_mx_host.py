@@ -132,3 +132,24 @@ def test_the_test_build_reaches_every_form_for_long_launches():
     assert lengths == {"ZDO_MX_WIDE_TILES", "ZDO_MX_LONG_TILES"}
     for name in lengths:
         assert f"-D{name}=1" in ZB.GRID_LOOP_FLAGS
+
+
+@pytest.mark.parametrize("buckets", [[], [(1, 1)], [(0, 0), (2, 2)], (1, 1), None])
+def test_a_list_without_buckets_is_checked_like_any_other(monkeypatch, buckets):
+    """The library's checks are made whatever the list holds: here the plan
+    has no device, which each call says."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    plan = Z.build_range_map([10] * 3, 10, 2, 0)
+    monkeypatch.setattr(ZM._Call, "ptr", lambda self, t, what, kind, numel: 1 << 20)
+    monkeypatch.setattr(ZM._Call, "storage", lambda self, mx, what, coords: (1 << 21, 1 << 22))
+    monkeypatch.setattr(ZM._Call, "inputs", lambda self, storages, what, coords: Z.MxBuffers([]))
+    monkeypatch.setattr(ZM._Call, "stream", lambda self, stream: 0)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+    for call in (lambda: Z.quantize_grads_mxfp4(plan, None, Z.WORLD, None, buckets=buckets),
+                 lambda: Z.reduce_scatter_local_mxfp4(plan, [], Z.LOCAL, 1.0, None, Z.LOCAL, buckets=buckets),
+                 lambda: Z.sharded_adam_step_mxfp4(plan, [], Z.LOCAL, 1.0, None, None, None, buckets=buckets, **hp)):
+        with pytest.raises(Z.ZdoError) as e:
+            call()
+        assert e.value.code == Z.EHIP

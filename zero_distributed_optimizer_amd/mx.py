@@ -161,6 +161,10 @@ class _Call:
                 runs.append((b, e))
         return runs
 
+    def launches(self, buckets):
+        """The ranges of `buckets`, or an empty one, for the library's checks."""
+        return self.buckets(buckets) or ((0, 0),)
+
 
 def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buckets=None, stream=None) -> None:
     """The bf16 gradient buffer to MXFP4, into the storage `out` (both in
@@ -173,7 +177,7 @@ def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buc
     r = call.opt(residual, "residual", "f32", n)
     c, s = call.storage(out, "out", coords)
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.buckets(buckets):
+    for b0, b1 in call.launches(buckets):
         _check(L.quantize_grads_mxfp4(plan.handle, b0, b1, g, coords, r, c, s, st))
 
 
@@ -186,7 +190,7 @@ def reduce_scatter_local_mxfp4(plan: Plan, contributions, coords: int, scale: fl
     mx = call.inputs(contributions, "contributions", coords)
     o = call.ptr(out, "out", "bf16", plan.extent(out_coords))
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.buckets(buckets):
+    for b0, b1 in call.launches(buckets):
         _check(L.reduce_scatter_local_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, o,
                                             out_coords, st))
 
@@ -225,7 +229,7 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     mg = call.opt(main_grad_out, "main_grad_out", "f32", L)
     hp = adam_hparams(lr, beta1, beta2, eps, weight_decay, step)
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.buckets(buckets):
+    for b0, b1 in call.launches(buckets):
         _check(L.sharded_adam_step_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, m, a, v, p,
                                          param_coords, pc, ps, param_mx_coords, ctypes.byref(hp), gc, mg, st))
 
