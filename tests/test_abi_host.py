@@ -213,3 +213,17 @@ def test_buffers_reject_host_tensors_and_wrong_dtypes():
         zdo.Buffers([np.zeros(8, np.int16)], "replicas")
     empty = zdo.Buffers([], "replicas")
     assert len(empty) == 0 and empty.numel == 0
+
+
+def test_the_current_stream_without_torchs_raw_handle(monkeypatch):
+    """The binding reads the current stream's handle by a function that is no
+    part of torch's interface, and without it by the one that is."""
+    import types
+
+    import torch
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=70 + device))
+    assert Z._stream(None, 3) == 73 and Z._stream(None, torch.device("cuda", 2)) == 72
+    assert Z._stream(types.SimpleNamespace(cuda_stream=9), 3) == 9
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 90 + device, raising=False)
+    assert Z._stream(None, 3) == 93 and Z._stream(None, torch.device("cuda", 2)) == 92

@@ -1033,3 +1033,28 @@ def test_d32_whole_tiles_and_edges(gpu, seed):
         c = gpu.WORLD if r % 2 else gpu.LOCAL
         run_rank_step(gpu, sizes, bucket, D, r, reps_h, state, 1.0 / D, hp, 5, c, gpu.LOCAL if r % 2 else gpu.WORLD)
     free()
+
+
+def test_calls_read_the_current_stream(gpu, monkeypatch):
+    """The binding's handle of the current stream is torch's, on the default
+    stream, on another and while one is captured, by either way of reading it."""
+    def check():
+        for device in (0, torch.device("cuda", 0)):
+            assert gpu._stream(None, device) == torch.cuda.current_stream().cuda_stream
+
+    def everywhere():
+        check()
+        side = torch.cuda.Stream()
+        assert gpu._stream(side, 0) == side.cuda_stream
+        with torch.cuda.stream(side):
+            check()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                check()
+                torch.zeros(1, device=DEV)
+        torch.cuda.synchronize()
+        del g
+
+    everywhere()
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    everywhere()

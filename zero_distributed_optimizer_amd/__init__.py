@@ -324,11 +324,14 @@ def _ptr_list(ts, what: str, numel: int):
 
 def _stream(stream, device) -> int:
     """The handle of `stream`, or of the current stream of `device` (a device
-    or its index), read by itself: torch.cuda.current_stream builds a Stream
-    object, which takes 1.9 us."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(device if isinstance(device, int) else device.index)
-    return stream.cuda_stream
+    or its index). torch's raw handle is read by itself where torch offers it
+    (it is no part of its interface): torch.cuda.current_stream builds a
+    Stream object, which takes 1.9 us."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch, index = _torch(), device if isinstance(device, int) else device.index
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(index).cuda_stream if raw is None else raw(index)
 
 
 def _bucket_list(buckets):
