@@ -28,7 +28,9 @@
  * A storage is two device arrays, both 16-byte aligned: codes (16 bytes a
  * block) and scales (1 byte a block), for zdo_plan_mx_blocks(plan, coords)
  * blocks. Plans of more than 2^30 tiles in a storage that a call uses are
- * refused with ZDO_EINVAL.
+ * refused with ZDO_EINVAL; all_gather_params_mxfp4, which walks every rank's
+ * ranges, refuses those of more than 2^30 in WORLD storage (D times the LOCAL
+ * ones), whatever its coordinates.
  *
  * Rounding to MXFP4, per block: A = max |x| over its slots;
  * e = max(0, X - 2), X the biased fp32 exponent of A (0 for subnormals), so
