@@ -77,8 +77,9 @@ int64_t zdo_plan_norm_mxfp4_workspace_bytes(const zdo_plan *plan);
  * x - value, the part that the 4 bits did not carry, to be sent with the
  * next step (exact in fp32: nothing is lost between them). A block whose x
  * holds an Inf or a NaN leaves its residual as it was. Only parameter
- * elements are read or rewritten. Outputs must not overlap each other or the
- * grads. */
+ * elements are read or rewritten. A contribution whose step is skipped is not
+ * sent again: only its residual is carried over. Outputs must not overlap each
+ * other or the grads. */
 int quantize_grads_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32_t bucket_end, const uint16_t *grads,
                          int32_t coords, float *residual, uint8_t *codes, uint8_t *scales, void *stream);
 
@@ -120,7 +121,11 @@ int grad_norm_sq_mxfp4(const zdo_plan *plan, const uint8_t *const *codes, const 
  *     rounded to MXFP4, storage in param_mx_coords, all blocks of the rank's
  *     ranges of those buckets written.
  * main_grad_out: NULL or fp32, L elements. The other arguments and rules as
- * sharded_adam_step; no output may overlap another or an input. */
+ * sharded_adam_step; no output may overlap another or an input.
+ * A skipped step leaves param_codes and param_scales as they were, and what
+ * they hold is gathered all the same: a storage is given its first contents by
+ * writeback_params_mxfp4, before any step (zeroed memory would be gathered as
+ * parameters of zero if the first step is skipped). */
 int sharded_adam_step_mxfp4(const zdo_plan *plan, int32_t bucket_begin, int32_t bucket_end,
                             const uint8_t *const *codes, const uint8_t *const *scales, int32_t n, int32_t coords,
                             float scale, float *master, float *exp_avg, float *exp_avg_sq, uint16_t *param_out,

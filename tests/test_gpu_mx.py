@@ -905,6 +905,26 @@ def test_overflow_skips_the_step(gpu):
     free()
 
 
+def test_overflow_in_the_first_step(gpu):
+    """The documented order: the parameters' storage is written once before
+    the first step, which is skipped; the gather then gives the parameters as
+    they are, and no zeros."""
+    loop = Loop(gpu, [5000, 17, 3000], 4000, 4)
+    d, o = loop.device(), loop.oracle()
+    for r in range(loop.D):
+        gpu.writeback_params_mxfp4(loop.plans[r], d["st"][r][0], d["par"][r], gpu.LOCAL)
+        MX.writeback(loop.lay, r, loop.state0[r][0], o["par"][r], MX.LOCAL)
+    MX.all_gather(loop.lay, o["par"], MX.LOCAL, o["out"])
+    d["grads"][1][77] = 0x7F80
+    loop.run(d, 1, 1.0)
+    assert torch.isnan(d["coeff"]).all() and np.count_nonzero(o["out"] & 0x7FFF) > 7000
+    assert_bf16(host_u16(d["out"]), o["out"], "gathered")
+    for r in range(loop.D):
+        for a, b in zip(d["st"][r], loop.state0[r]):
+            assert np.array_equal(host_f32(a).view(np.uint32), b.view(np.uint32))
+    free()
+
+
 def test_two_graphs_replay_as_the_eager_loop(gpu):
     """Two captured loops with buffers of their own, replayed in turn with
     eager work between; every replay equals the eager loop."""

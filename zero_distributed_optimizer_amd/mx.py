@@ -5,7 +5,9 @@ marshal arguments; every step of the work runs in the library's kernels.
 A storage is a pair (codes, scales) of uint8 device tensors, 16 bytes and 1
 byte for each of plan.mx_blocks(coords) blocks; mx_empty makes one.
 
-    mx = mx_empty(plan, WORLD)
+    mx, mine = mx_empty(plan, WORLD), mx_empty(plan, LOCAL)
+    writeback_params_mxfp4(plan, master, mine, LOCAL)   # once: a skipped step leaves it as it is
+    # every step:
     quantize_grads_mxfp4(plan, grads, WORLD, mx, residual=residual)
     # the ranks exchange their storages' ranges; then the owner of a range:
     sharded_adam_step_mxfp4(plan, contributions, LOCAL, scale, master, exp_avg, exp_avg_sq,
@@ -216,8 +218,9 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     """sharded_adam_step on contributions in MXFP4 (storages in `coords`). The
     updated parameters go to param_out (bf16) and, rounded to MXFP4, to the
     storage param_mx. grad_coeff: a one-element float32 device tensor that
-    multiplies the main grad (NaN skips the step). buckets: as
-    quantize_grads_mxfp4."""
+    multiplies the main grad (NaN skips the step, and leaves param_out and
+    param_mx as they were: writeback_params_mxfp4 gives param_mx its first
+    contents). buckets: as quantize_grads_mxfp4."""
     call, L = _Call(plan), plan.shard_numel
     mx = call.inputs(contributions, "contributions", coords)
     m = call.ptr(master, "master", "f32", L)
