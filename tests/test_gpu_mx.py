@@ -267,6 +267,61 @@ def test_values_of_every_code_and_scale(either):
     assert_bf16(host_u16(out), want, "gather")
 
 
+def test_every_pair_of_codes_and_scale(either):
+    """All 256 bytes of codes at all 256 scales: their values in fp32 (the
+    step's main grad) and in bf16 (the gather)."""
+    gpu = either
+    n = 256 * 512
+    lay = OL.build_layout([n], n, 1)
+    plan = gpu.build_range_map([n], n, 1, 0)
+    s = MX.empty(lay, gpu.LOCAL)
+    s[0][:4096] = np.tile(np.arange(256, dtype=np.uint8), 256).reshape(4096, 16)
+    s[1][:4096] = np.repeat(np.arange(256), 16)
+    with np.errstate(over="ignore"):
+        want = MX.decode(s[0][:4096], s[1][:4096]).reshape(-1).astype(np.float32)
+    st = [torch.ones(n, device=DEV) for _ in range(3)]
+    g, out = torch.zeros(n, device=DEV), torch.zeros(n, dtype=torch.int16, device=DEV)
+    gpu.sharded_adam_step_mxfp4(plan, [dev_mx(s)], gpu.LOCAL, 1.0, *st, main_grad_out=g,
+                                **hp_kwargs(W.get("tiny").hp, 1))
+    gpu.all_gather_params_mxfp4(plan, [dev_mx(s)], gpu.LOCAL, out)
+    assert_f32(host_f32(g), want, "fp32")
+    assert np.array_equal(np.signbit(host_f32(g))[~np.isnan(want)], np.signbit(want)[~np.isnan(want)])
+    assert_bf16(host_u16(out), ON.narrow(want), "bf16")
+
+
+@pytest.mark.parametrize("top", ["any", 0, 1, 3, 40, 100, 127, 150, 200, 254])
+def test_rounding_of_random_fp32(gpu, top):
+    """2^20 fp32 of random bits, by themselves and below one element of a
+    block that sets its scale from exponent field `top` (0: its subnormals),
+    beside every border between two codes and its neighbours, both signs."""
+    n = 1 << 20
+    rng = np.random.default_rng(5)
+    x = rng.integers(0, 1 << 32, n, dtype=np.uint32).view(np.float32)
+    if top != "any":
+        y = np.abs(x)
+        unit = np.float32(np.ldexp(1.0, max(top, 1) - 127 - 2))   # the block's largest lies in [4, 8) of it
+        with np.errstate(invalid="ignore"):
+            x = np.where((y < 8 * unit.astype(np.float64)) & np.isfinite(x), x, rng.uniform(-6, 6, n) * unit)
+        x = x.astype(np.float32)
+        if top == 0:
+            x = np.where(np.abs(x) < np.float32(2.0**-126), x, np.float32(0)).astype(np.float32)
+        t = np.array([0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7, 7.5], np.float64) * unit
+        t = t[(t >= 2.0**-149) & (t < (2.0**-126 if top == 0 else np.inf))].astype(np.float32)
+        near = np.concatenate([t, np.nextafter(t, np.float32(0)), np.nextafter(t, np.float32(np.inf))])
+        if top == 0:
+            near = near[near < np.float32(2.0**-126)]
+        near = np.concatenate([near, -near])
+        at = rng.permutation(n // 32)[:near.size]
+        x[32 * at + 1 + rng.integers(0, 31, near.size)] = near
+        x[::32] = np.float32(2.0**-127) if top == 0 else 4 * unit
+    lay = OL.build_layout([n], n, 1)
+    plan = gpu.build_range_map([n], n, 1, 0)
+    want, got = MX.empty(lay, MX.LOCAL), gpu.mx_empty(plan, gpu.LOCAL)
+    MX.writeback(lay, 0, x, want, MX.LOCAL)
+    gpu.writeback_params_mxfp4(plan, to_dev(x), got, gpu.LOCAL)
+    assert_mx(got, want, f"top {top}")
+
+
 @pytest.mark.parametrize("n", [1, 2, 3, 8, 13, 16, 32, 45])
 def test_long_reductions(gpu, n):
     """20 M slots in ragged buckets: the forms for long launches, reduction and
