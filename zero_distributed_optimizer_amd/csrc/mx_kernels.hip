@@ -10,10 +10,10 @@
 //
 // gfx950 converts between fp32 and E2M1 pairs with the block's scale in one
 // instruction (v_cvt_scalef32_pk_f32_fp4, v_cvt_scalef32_pk_fp4_f32), the
-// scale given as an fp32 whose exponent field is the E8M0 byte. Checked on
-// the device over all 256 scales x 256 pairs, and over every bf16 and 2^20
-// random fp32 values: exact, subnormal results kept, scale 255 gives NaN,
-// rounding to nearest even and saturating at 6.
+// scale given as an fp32 whose exponent field is the E8M0 byte. The tests
+// hold them to the oracle over all 256 scales x 256 pairs, every bf16, and
+// 2^20 random fp32 at ten scales: exact, subnormal results kept, scale 255
+// gives NaN, rounding to nearest even and saturating at 6.
 #include <hip/hip_runtime.h>
 
 #include "device.h"
@@ -403,9 +403,13 @@ __device__ __forceinline__ void put_partial(double *at, double s) {
 // As the reductions, but with at most kMxNormWaves waves, each of which takes
 // every kMxNormWaves-th tile or unit and adds its lanes once at the end. A wave a
 // unit spent its time filling and in the butterfly: 3e8 slots of 1
-// contribution 62 us instead of 119, of 3 92 instead of 138, 5e8 of 16 663
-// instead of 694, GPT-2 small rank 19.7 instead of 21.9 (with 8192 waves
-// 64, 96, 668 and 19.8 us, with 4096 70, 99, 681 and 20.5).
+// contribution 62 us instead of 119, of 3 92 instead of 138, 5e8 of 16 688
+// instead of 694, GPT-2 small rank 20.8 instead of 21.9. With 16384, 8192 and
+// 4096 waves, in turn on another box: 62.9, 64.7 and 70.5 us, 92.0, 96.7 and
+// 99.8, 671, 675 and 687, 20.7, 20.0 and 21.4; 1e8 of 4 52.1, 50.2 and 50.2.
+// HBM bounds it from 8 contributions (8 of 3e8 213 us, 5.97 TB/s); with fewer,
+// vector instructions: of 1 contribution 5.3 an element for half a byte, whose
+// issue alone takes 60% of 63 us.
 __global__ __launch_bounds__(kBlock) void mx_norm_kernel(MxNormArgs a) {
     Squares s;
     for (int64_t i = blockIdx.x; i < a.walk.count; i += gridDim.x)
@@ -855,6 +859,14 @@ hipError_t launch_mx_norm(const MxNormArgs &args, double *norm_sq, hipStream_t s
     return hipGetLastError();
 }
 
+// Counts of contributions that have a kernel of their own: 8 and 16, the usual
+// ones of a node and of two. Against the kernel for any count, long launches:
+// 8 4960 us instead of 5063, 16 2906 instead of 3044. 2, 3, 4 and 12 would gain
+// 2 to 3% (3e8 slots of 2 1321 instead of 1358, of 3 1362 and 1399, of 4 1393
+// and 1432, 1.5e8 of 12 783 and 797; 8e6 of 4 40.2 and 42.8, but 2e6 of 4 12.3
+// and 11.2) at two more kernels each and are left to the one for any count; 1,
+// 24 and 32 would lose (1314 and 1308, 9e7 of 24 610 and 591, 2.5e8 of 32 1913
+// and 1826).
 // Waves that share a compute unit in the step. Long launches, Llama-3-8B
 // shapes: 8 contributions with all loads in flight 4809 us at 9 waves (8:
 // 4802, 10: 5227, 12: 5404, 6: 5901), 16 2871 us (8: 2875, 12: 2882); other
