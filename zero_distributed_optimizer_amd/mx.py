@@ -27,6 +27,7 @@ from . import (EINVAL, LOCAL, WORLD, Adam, Plan, ZdoError, _bucket_list, _check,
 MX_BUCKET_DTYPE = np.dtype([("block0", "<i8"), ("blocks", "<i8")])
 BLOCK = 32                # elements that share a scale
 CODE_BYTES = BLOCK // 2   # a block's codes
+NO_BUCKETS = ((0, 0),)    # an empty range, for the library's checks
 
 # Every symbol include/zdo_mx.h declares.
 MX_EXPORTS = ("zdo_plan_mx_blocks", "zdo_plan_mx_buckets", "zdo_plan_norm_mxfp4_workspace_bytes",
@@ -163,10 +164,6 @@ class _Call:
                 runs.append((b, e))
         return runs
 
-    def launches(self, buckets):
-        """The ranges of `buckets`, or an empty one, for the library's checks."""
-        return self.buckets(buckets) or ((0, 0),)
-
 
 def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buckets=None, stream=None) -> None:
     """The bf16 gradient buffer to MXFP4, into the storage `out` (both in
@@ -179,7 +176,7 @@ def quantize_grads_mxfp4(plan: Plan, grads, coords: int, out, residual=None, buc
     r = call.opt(residual, "residual", "f32", n)
     c, s = call.storage(out, "out", coords)
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.launches(buckets):
+    for b0, b1 in call.buckets(buckets) or NO_BUCKETS:
         _check(L.quantize_grads_mxfp4(plan.handle, b0, b1, g, coords, r, c, s, st))
 
 
@@ -192,7 +189,7 @@ def reduce_scatter_local_mxfp4(plan: Plan, contributions, coords: int, scale: fl
     mx = call.inputs(contributions, "contributions", coords)
     o = call.ptr(out, "out", "bf16", plan.extent(out_coords))
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.launches(buckets):
+    for b0, b1 in call.buckets(buckets) or NO_BUCKETS:
         _check(L.reduce_scatter_local_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, o,
                                             out_coords, st))
 
@@ -232,7 +229,7 @@ def sharded_adam_step_mxfp4(plan: Plan, contributions, coords: int, scale: float
     mg = call.opt(main_grad_out, "main_grad_out", "f32", L)
     hp = adam_hparams(lr, beta1, beta2, eps, weight_decay, step)
     st, L = call.stream(stream), require_library()
-    for b0, b1 in call.launches(buckets):
+    for b0, b1 in call.buckets(buckets) or NO_BUCKETS:
         _check(L.sharded_adam_step_mxfp4(plan.handle, b0, b1, mx.codes, mx.scales, len(mx), coords, scale, m, a, v, p,
                                          param_coords, pc, ps, param_mx_coords, ctypes.byref(hp), gc, mg, st))
 
