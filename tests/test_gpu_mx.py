@@ -749,6 +749,32 @@ def test_per_bucket_calls_equal_the_whole(gpu):
     free()
 
 
+@pytest.mark.parametrize("coords", [0, 1])
+def test_bucket_lists_of_quantize_and_reduce(gpu, coords):
+    """Lists of buckets in any order, those that touch and those that do not,
+    against the oracle bucket by bucket; what no list names stays."""
+    sizes, bucket, D, r = [5000, 77, 9000, 1400, 1500, 1600, 2000, 3000], 1500, 4, 2
+    lay = OL.build_layout(sizes, bucket, D)
+    plan = gpu.build_range_map(sizes, bucket, D, r)
+    rng, nb = np.random.default_rng(8), plan.num_buckets
+    n = lay.buffer_numel if coords == gpu.WORLD else plan.shard_numel
+    g, res0 = bf16_host(rng, n), (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    stores, dev = sources(gpu, rng, lay, r, 3, coords)
+    assert nb >= 6
+    for lists in ([(4, 6), (0, 1), (1, 2)], [(nb - 1, nb), (2, 2), (1, 3)], [(0, nb)], []):
+        want, want_res, got, res = MX.empty(lay, coords, FILL), res0.copy(), dev_mx(MX.empty(lay, coords, FILL)), to_dev(res0)
+        wout, out = np.full(n, SENTINEL, np.uint16), torch.full((n,), SENTINEL, dtype=torch.int16, device=DEV)
+        for b in lists:
+            MX.quantize(lay, r, g, coords, want, want_res, b)
+            MX.reduce_scatter(lay, r, stores, coords, 0.3, wout, coords, b)
+        gpu.quantize_grads_mxfp4(plan, to_dev(g), coords, got, residual=res, buckets=lists)
+        gpu.reduce_scatter_local_mxfp4(plan, dev, coords, 0.3, out, coords, buckets=lists)
+        assert_mx(got, want, f"{lists}")
+        assert np.array_equal(host_f32(res).view(np.uint32), want_res.view(np.uint32))
+        assert_bf16(host_u16(out), wout, f"{lists}")
+    free()
+
+
 # ---- parameters ------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("coords", [0, 1])
