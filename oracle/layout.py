@@ -19,7 +19,7 @@ distributed optimizer chapter):
     r * (bucket size / D) within the bucket.
   * §5: padding that makes a bucket divisible by D belongs to the buffer layout.
 
-Readings where the page leaves a step open (each also listed in the design doc):
+Readings where the page leaves a step open:
   * A parameter belongs to exactly one bucket (§4.1 speaks of "its" bucket);
     buckets are filled greedily in parameter order and a bucket closes right
     after the parameter that brings its element count to at least
