@@ -405,7 +405,7 @@ __device__ __forceinline__ void put_partial(double *at, double s) {
 // unit spent its time filling and in the butterfly: 3e8 slots of 1
 // contribution 62 us instead of 119, of 3 92 instead of 138, 5e8 of 16 688
 // instead of 694, GPT-2 small rank 20.8 instead of 21.9. With 16384, 8192 and
-// 4096 waves, in turn on another box: 62.9, 64.7 and 70.5 us, 92.0, 96.7 and
+// 4096 waves, in turn in a later run: 62.9, 64.7 and 70.5 us, 92.0, 96.7 and
 // 99.8, 671, 675 and 687, 20.7, 20.0 and 21.4; 1e8 of 4 52.1, 50.2 and 50.2.
 // HBM bounds it from 8 contributions (8 of 3e8 213 us, 5.97 TB/s); with fewer,
 // vector instructions: of 1 contribution 5.3 an element for half a byte, whose
