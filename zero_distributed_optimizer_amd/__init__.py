@@ -12,7 +12,8 @@ implementation.
                       param_buffer, WORLD, lr=..., beta1=..., ..., step=t)
 
 The calls with contributions and parameters in 4 bits (include/zdo_mx.h) are in
-mx.py and reached from here as well.
+mx.py, those at the vocabulary matrix (include/zdo_vocab.h) in vocab.py; both
+are reached from here as well.
 """
 
 from __future__ import annotations
@@ -143,6 +144,7 @@ def require_library() -> ctypes.CDLL:
               "reduce_scatter_local_bucket_list", "sharded_adam_step_bucket_list", "zdo_stream_probe"):
         getattr(L, f).restype = ctypes.c_int
     mx.declare(L)
+    vocab.declare(L)
     _lib = L
     return L
 
@@ -519,6 +521,8 @@ def stream_probe(reads, state, out, n: int, waves_per_cu: int = 0, stream=None, 
                                               _stream(stream, out.device)))
 
 
-from . import mx  # noqa: E402  (it uses the names above)
+from . import mx, vocab  # noqa: E402  (they use the names above)
 from .mx import (MxBuffers, all_gather_params_mxfp4, grad_norm_sq_mxfp4, mx_empty,  # noqa: E402,F401
                  quantize_grads_mxfp4, reduce_scatter_local_mxfp4, sharded_adam_step_mxfp4, writeback_params_mxfp4)
+from .vocab import (BF16, F32, embedding_grad, embedding_grad_workspace_bytes, embedding_lookup,  # noqa: E402,F401
+                    linear_cross_entropy, linear_cross_entropy_grad, linear_cross_entropy_workspace_bytes)

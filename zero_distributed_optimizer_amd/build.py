@@ -24,8 +24,9 @@ LIB = os.path.join(HERE, "libzdo.so")
 # and steps take their forms for long launches at any length.
 GRID_LOOP_LIB = os.path.join(HERE, "libzdo_gridloop.so")
 GRID_LOOP_FLAGS = ["-DZDO_MAX_GRID=64", "-DZDO_MX_WIDE_TILES=1", "-DZDO_MX_LONG_TILES=1"]
-SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "mx_abi.cpp", "mx_kernels.hip"]
-HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h"]
+SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "mx_abi.cpp", "mx_kernels.hip", "vocab_abi.cpp", "vocab_kernels.hip",
+           "vocab_gemm.hip"]
+HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h", "vocab.h"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -39,7 +40,7 @@ FLAGS = [
 
 def sources() -> list[str]:
     return [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS] + \
-        [os.path.join(INCLUDE, "zdo.h"), os.path.join(INCLUDE, "zdo_mx.h")]
+        [os.path.join(INCLUDE, h) for h in ("zdo.h", "zdo_mx.h", "zdo_vocab.h")]
 
 
 def build(verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:

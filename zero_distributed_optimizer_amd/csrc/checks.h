@@ -75,6 +75,46 @@ inline int check_buckets(const zdo_plan *plan, int32_t b0, int32_t b1, const cha
     return ZDO_OK;
 }
 
+// A call's body: no exception leaves the C entry.
+template <typename F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (...) {
+        set_error("out of memory");   // short enough to need no allocation
+        return ZDO_ENOMEM;
+    }
+}
+
+// The buffers of one call: what it writes must not overlap anything else of
+// it.
+struct Buffers {
+    static constexpr int kMaxReads = 2 * ZDO_MAX_REPLICAS + 2, kMaxWrites = 8;
+    Span read[kMaxReads], write[kMaxWrites];
+    const char *read_name[kMaxReads], *write_name[kMaxWrites];
+    int nread = 0, nwrite = 0;
+
+    void reads(Span s, const char *name) {
+        read[nread] = s;
+        read_name[nread++] = name;
+    }
+    void writes(Span s, const char *name) {
+        write[nwrite] = s;
+        write_name[nwrite++] = name;
+    }
+    int check(const char *fn) const {
+        for (int i = 0; i < nwrite; ++i) {
+            for (int k = i + 1; k < nwrite; ++k)
+                if (overlap(write[i], write[k]))
+                    return fail(ZDO_EALIAS, std::string(fn) + ": " + write_name[i] + " overlaps " + write_name[k]);
+            for (int k = 0; k < nread; ++k)
+                if (overlap(write[i], read[k]))
+                    return fail(ZDO_EALIAS, std::string(fn) + ": " + write_name[i] + " overlaps " + read_name[k]);
+        }
+        return ZDO_OK;
+    }
+};
+
 // Adam's hyper-parameters (abi.cpp): their checks, and the constants of one
 // step.
 int check_adam(const zdo_adam *hp, const char *fn);

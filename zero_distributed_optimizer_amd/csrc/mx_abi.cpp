@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <new>
 #include <string>
 
 #include "checks.h"
@@ -13,17 +12,6 @@
 
 namespace zdo {
 namespace {
-
-// A call's body: no exception leaves the C entry.
-template <typename F>
-int guarded(F body) {
-    try {
-        return body();
-    } catch (...) {
-        set_error("out of memory");   // short enough to need no allocation
-        return ZDO_ENOMEM;
-    }
-}
 
 int64_t mx_tiles(const zdo_plan *p, int32_t coords) { return p->mx_tiles * (coords == ZDO_WORLD ? p->dp_size : 1); }
 
@@ -39,35 +27,6 @@ int check_storage(const zdo_plan *p, int32_t coords, const char *fn, const char 
                                     std::to_string(kMxMaxTiles));
     return ZDO_OK;
 }
-
-// The buffers of one call: what it writes must not overlap anything else of
-// it.
-struct Buffers {
-    static constexpr int kMaxReads = 2 * ZDO_MAX_REPLICAS + 2, kMaxWrites = 8;
-    Span read[kMaxReads], write[kMaxWrites];
-    const char *read_name[kMaxReads], *write_name[kMaxWrites];
-    int nread = 0, nwrite = 0;
-
-    void reads(Span s, const char *name) {
-        read[nread] = s;
-        read_name[nread++] = name;
-    }
-    void writes(Span s, const char *name) {
-        write[nwrite] = s;
-        write_name[nwrite++] = name;
-    }
-    int check(const char *fn) const {
-        for (int i = 0; i < nwrite; ++i) {
-            for (int k = i + 1; k < nwrite; ++k)
-                if (overlap(write[i], write[k]))
-                    return fail(ZDO_EALIAS, std::string(fn) + ": " + write_name[i] + " overlaps " + write_name[k]);
-            for (int k = 0; k < nread; ++k)
-                if (overlap(write[i], read[k]))
-                    return fail(ZDO_EALIAS, std::string(fn) + ": " + write_name[i] + " overlaps " + read_name[k]);
-        }
-        return ZDO_OK;
-    }
-};
 
 // n storages to be read.
 int take_inputs(const zdo_plan *p, const uint8_t *const *codes, const uint8_t *const *scales, int32_t n,

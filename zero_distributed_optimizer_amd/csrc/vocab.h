@@ -1,0 +1,219 @@
+// Launch arguments, workspace layouts and launchers of the vocabulary
+// matrix's kernels (vocab_kernels.hip, vocab_gemm.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "zdo_internal.h"
+
+namespace zdo {
+
+constexpr int64_t kVocabMaxN = int64_t(1) << 30;
+constexpr int64_t kCeMaxN = int64_t(1) << 22;  // rows of d^T: 256 of them within 32 bits of bytes
+constexpr int64_t kVocabMaxRows = int64_t(1) << 30;
+constexpr int64_t kVocabMaxDim = int64_t(1) << 20;
+constexpr int64_t kVocabMaxStride = int64_t(1) << 30;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// ---- embedding -------------------------------------------------------------------
+
+struct LookupArgs {
+    const uint16_t *w;  // row 0
+    int64_t vocab, dim;
+    const int64_t *tokens;
+    int64_t n;
+    float scale;
+    void *out;
+    int32_t f32;
+    int64_t stride;
+};
+
+// A row's sum takes whole chunks of this many sorted positions from the sums
+// that a kernel of its own has left; a run of one token is thus split over
+// many waves, and in the same places whatever else the batch holds.
+constexpr int kRunChunk = 64;
+
+struct RowsArgs {
+    uint16_t *g;  // the parameter's first element
+    int64_t numel, vocab, dim;
+    const int64_t *tokens;
+    int64_t n;
+    const void *x;
+    int32_t f32;
+    int64_t stride;
+    float scale;
+    int32_t accumulate;
+    void *workspace;
+};
+
+// Up to this many positions are sorted by counting, in one launch (see
+// rank_kernel); more by digits.
+constexpr int64_t kRankMax = 8192;
+// Sorting by digits: positions a workgroup takes, and most bins of a digit.
+constexpr int kSortItems = 4096;
+constexpr int kSortBins = 512;
+
+// The workspace of embedding_grad. Keys and positions lie in two sets, from
+// one to the other a pass.
+struct RowsLayout {
+    int64_t blocks, chunks;
+    int64_t key[2], pos[2], hist, partial, bytes;
+};
+
+inline RowsLayout rows_layout(int64_t n, int64_t dim) {
+    RowsLayout l{};
+    l.blocks = ceil_div(n, kSortItems);
+    l.chunks = n / kRunChunk;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    for (int i = 0; i < 2; ++i) {
+        l.key[i] = take(4 * n);
+        l.pos[i] = take(4 * n);
+    }
+    l.hist = take(n > kRankMax ? 4 * kSortBins * l.blocks : 0);
+    l.partial = take(4 * l.chunks * dim);
+    l.bytes = std::max<int64_t>(at, 256);
+    return l;
+}
+
+// ---- cross entropy -----------------------------------------------------------------
+
+// C[m][n] = sum over k of A[m][k] B[n][k], in tiles (vocab_gemm.hip). A and B
+// are bf16 rows, 16-byte aligned, strides of a multiple of 8 elements, K a
+// multiple of kDepth. What becomes of C is the epilogue's.
+constexpr int kDepth = 64;
+
+enum Epilogue : int { kScore, kDiff, kSum, kRows };
+
+struct GemmArgs {
+    const uint16_t *a, *b;
+    int64_t lda, ldb;
+    int64_t m, n, k;
+    int32_t splits;  // of k, each with an output of its own (kSum)
+
+    // kScore, kDiff: m are a piece's rows of W, n tokens
+    const int64_t *targets;
+    int64_t row0;  // the piece's first row
+    int64_t vocab;
+    // kScore: per tile of rows and token the largest logit and the sum of
+    // exp(logit - it), and the target's logit
+    float2 *part;
+    int64_t tile0;  // the piece's first tile
+    float *pick;
+    // kDiff: d in both orders, zero up to the next multiple of kDepth of the
+    // other index
+    const float *lse, *weight;
+    uint16_t *d, *dt;
+    int64_t ldd, lddt;
+
+    // kSum: fp32 [split][n][lds], added to what is there unless `first`
+    float *sum;
+    int64_t lds;
+    int32_t first;
+
+    // kRows: bf16 rows n of m elements
+    uint16_t *rows;
+    int32_t accumulate;
+};
+
+// Tiles are 256 x 256 where those are enough to occupy the chip's 256 compute
+// units, else 128 x 128. The partial results of kScore are laid out for the
+// smaller ones.
+constexpr int kTileRowsMin = 128;
+inline bool wide_tiles(int64_t m, int64_t n, int64_t splits) {
+    return ceil_div(m, 256) * ceil_div(n, 256) * splits >= 192;
+}
+inline int64_t tile_rows(int64_t m, int64_t n) { return wide_tiles(m, n, 1) ? 256 : kTileRowsMin; }
+
+// A call's workspace. The vocabulary is taken in pieces of `piece` rows.
+// (elements of d in one order: at most 2^26, 128 MB, so that both orders stay
+// in the 256 MB Infinity Cache between the product that writes them and the
+// two that read them, but at least 256 rows; of the piece's copies of W: at
+// most 2^27).
+struct CeLayout {
+    int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
+    int64_t splits;                   // of grad_hidden's sum
+    int64_t hidden, hidden_t, w, w_t, d, d_t, sum, part, pick, bytes;
+};
+
+// Splits of the sum over the vocabulary that grad_hidden is: as many as give
+// the chip's 256 compute units a tile each, but steps of at least 16 * kDepth
+// rows.
+inline int64_t hidden_splits(int64_t n, int64_t dim, int64_t piece) {
+    const int64_t tiles = ceil_div(n, 256) * ceil_div(dim, 256);
+    return std::max<int64_t>(1, std::min(256 / tiles, piece / (16 * kDepth)));
+}
+
+inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
+    CeLayout l{};
+    l.kdim = round_up(dim, kDepth);
+    l.npad = round_up(std::max<int64_t>(n, 1), kDepth);
+    int64_t most = std::min((int64_t(1) << 26) / l.npad, (int64_t(1) << 27) / l.kdim);
+    most = std::max<int64_t>(256, most / 256 * 256);
+    const int64_t pieces = ceil_div(vocab, most);
+    l.piece = std::min(vocab, round_up(ceil_div(vocab, pieces), 256));
+    l.vpad = round_up(l.piece, kDepth);
+    l.splits = hidden_splits(std::max<int64_t>(n, 1), dim, l.piece);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    l.hidden = take(2 * n * l.kdim);
+    l.w = take(2 * l.piece * l.kdim);
+    const int64_t both = at;
+    // the loss
+    l.part = take(8 * n * (ceil_div(vocab, l.piece) * ceil_div(l.piece, kTileRowsMin)));
+    l.pick = take(4 * n);
+    const int64_t loss = at;
+    // its gradient
+    at = both;
+    l.hidden_t = take(2 * dim * l.npad);
+    l.w_t = take(2 * dim * l.vpad);
+    l.d = take(2 * n * l.vpad);
+    l.d_t = take(2 * l.piece * l.npad);
+    l.sum = take(4 * l.splits * n * l.kdim);
+    l.bytes = std::max<int64_t>(std::max(at, loss), 256);
+    return l;
+}
+
+struct CeArgs {
+    const uint16_t *w;  // row 0
+    int64_t vocab, dim;
+    const uint16_t *hidden;
+    int64_t hidden_stride;
+    const int64_t *targets;
+    int64_t n;
+    float *loss;     // the loss: written
+    float *lse;      // the loss: written; the gradient: read
+    // the gradient
+    const float *grad_loss;
+    void *grad_hidden;  // may be NULL
+    int32_t f32;
+    int64_t grad_hidden_stride;
+    uint16_t *grads;  // the parameter's first element; may be NULL
+    int64_t numel;    // the parameter's
+    int32_t accumulate;
+    char *workspace;
+};
+
+hipError_t launch_lookup(const LookupArgs &a, hipStream_t stream);
+hipError_t launch_rows(const RowsArgs &a, hipStream_t stream);
+hipError_t launch_ce(const CeArgs &a, hipStream_t stream);
+hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream);
+hipError_t launch_gemm(Epilogue e, const GemmArgs &a, hipStream_t stream);
+
+// Elements [0, n) to zero.
+hipError_t launch_zero(uint16_t *p, int64_t n, hipStream_t stream);
+
+}  // namespace zdo
