@@ -33,10 +33,11 @@ struct LookupArgs {
     int64_t stride;
 };
 
-// A row's sum takes whole chunks of this many sorted positions from the sums
-// that a kernel of its own has left; a run of one token is thus split over
-// many waves, and in the same places whatever else the batch holds.
-constexpr int kRunChunk = 64;
+// Sorted positions that a wave sums (see runs_kernel): at most its 64 lanes;
+// with few positions fewer each, so that the chip has waves enough (8,192
+// tokens of GPT-2 small: 8.4 us by 8, 11.6 by 16, 19 by 32; 131,072: the sums
+// take the same at 16 and 64, and joining the parts 39 us at 16, 13 at 64).
+inline int rows_chunk(int64_t n) { return n >= 65536 ? 64 : n >= 32768 ? 32 : n >= 16384 ? 16 : 8; }
 
 struct RowsArgs {
     uint16_t *g;  // the parameter's first element
@@ -54,21 +55,26 @@ struct RowsArgs {
 // Up to this many positions are sorted by counting, in one launch (see
 // rank_kernel); more by digits.
 constexpr int64_t kRankMax = 8192;
-// Sorting by digits: positions a workgroup takes, and most bins of a digit.
-constexpr int kSortItems = 4096;
+// Sorting by digits: positions a workgroup takes (few, so that there are
+// workgroups enough; more where the scan of a digit's counts would weigh), and
+// most bins of a digit.
+inline int sort_items(int64_t n) { return n <= (int64_t(1) << 20) ? 1024 : 8192; }
 constexpr int kSortBins = 512;
 
 // The workspace of embedding_grad. Keys and positions lie in two sets, from
 // one to the other a pass.
 struct RowsLayout {
     int64_t blocks, chunks;
-    int64_t key[2], pos[2], hist, partial, bytes;
+    int32_t chunk, items;
+    int64_t key[2], pos[2], hist, part, bytes;
 };
 
 inline RowsLayout rows_layout(int64_t n, int64_t dim) {
     RowsLayout l{};
-    l.blocks = ceil_div(n, kSortItems);
-    l.chunks = n / kRunChunk;
+    l.items = sort_items(n);
+    l.blocks = ceil_div(n, l.items);
+    l.chunk = rows_chunk(n);
+    l.chunks = ceil_div(n, l.chunk);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -79,8 +85,8 @@ inline RowsLayout rows_layout(int64_t n, int64_t dim) {
         l.key[i] = take(4 * n);
         l.pos[i] = take(4 * n);
     }
-    l.hist = take(n > kRankMax ? 4 * kSortBins * l.blocks : 0);
-    l.partial = take(4 * l.chunks * dim);
+    l.hist = take(n > kRankMax ? 4 * kSortBins * (l.blocks + 1) : 0);
+    l.part = take(4 * 2 * l.chunks * dim);
     l.bytes = std::max<int64_t>(at, 256);
     return l;
 }

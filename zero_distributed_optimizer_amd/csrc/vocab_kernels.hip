@@ -14,104 +14,119 @@
 namespace zdo {
 namespace {
 
-struct __attribute__((packed, aligned(2))) Loose16 {
-    u32x4 v;
+typedef u32x4 loose_u32x4 __attribute__((aligned(2)));
+typedef u32x2 loose_u32x2 __attribute__((aligned(2)));
+typedef f32x4 loose_f32x4 __attribute__((aligned(4)));
+
+// P consecutive elements of a row, widened: those of a 16-byte access, or 1
+// where a row has fewer.
+template <int P>
+struct Some {
+    float v[P];
 };
-struct __attribute__((packed, aligned(4))) LooseF4 {
-    f32x4 v;
-};
 
-// 8 elements of a row, or the first `count` of them and zeros.
-struct Eight {
-    float v[8];
-};
-
-__device__ __forceinline__ Eight widen(u32x4 x) {
-    return {{lo_f32(x.x), hi_f32(x.x), lo_f32(x.y), hi_f32(x.y), lo_f32(x.z), hi_f32(x.z), lo_f32(x.w), hi_f32(x.w)}};
-}
-
-__device__ __forceinline__ Eight read8(const uint16_t *p, int count) {
-    if (count >= 8)
-        return widen(reinterpret_cast<const Loose16 *>(p)->v);
-    Eight e{};
-    for (int i = 0; i < 7; ++i)
-        if (i < count)
-            e.v[i] = h_f32(p[i]);
-    return e;
-}
-
-__device__ __forceinline__ Eight read8(const float *p, int count) {
-    Eight e{};
-    if (count >= 8) {
-        const f32x4 a = reinterpret_cast<const LooseF4 *>(p)->v, b = reinterpret_cast<const LooseF4 *>(p + 4)->v;
-        for (int i = 0; i < 4; ++i) {
-            e.v[i] = a[i];
-            e.v[4 + i] = b[i];
-        }
-        return e;
-    }
-    for (int i = 0; i < 7; ++i)
-        if (i < count)
-            e.v[i] = p[i];
-    return e;
-}
-
-__device__ __forceinline__ void write8(uint16_t *p, const Eight &e, int count) {
-    u32x4 x;
-    for (int i = 0; i < 4; ++i)
-        x[i] = to_bf16x2(e.v[2 * i], e.v[2 * i + 1]);
-    if (count >= 8)
-        reinterpret_cast<Loose16 *>(p)->v = x;
+// kOnce: non-temporally, for what a launch reads once and in no order of
+// addresses (131,072 fp32 rows of 1024 by token: 101 us, 121 without).
+template <bool kOnce, typename V>
+__device__ __forceinline__ V load_as(const void *p) {
+    if constexpr (kOnce)
+        return __builtin_nontemporal_load(static_cast<const V *>(p));
     else
-        for (int i = 0; i < 7; ++i)
-            if (i < count)
-                p[i] = uint16_t(x[i >> 1] >> (i & 1) * 16);
+        return *static_cast<const V *>(p);
 }
 
-__device__ __forceinline__ void write8(float *p, const Eight &e, int count) {
-    if (count >= 8) {
-        reinterpret_cast<LooseF4 *>(p)->v = f32x4{e.v[0], e.v[1], e.v[2], e.v[3]};
-        reinterpret_cast<LooseF4 *>(p + 4)->v = f32x4{e.v[4], e.v[5], e.v[6], e.v[7]};
+template <int P, bool kOnce = false>
+__device__ __forceinline__ Some<P> load_some(const uint16_t *p) {
+    if constexpr (P == 8) {
+        const u32x4 x = load_as<kOnce, loose_u32x4>(p);
+        return {{lo_f32(x.x), hi_f32(x.x), lo_f32(x.y), hi_f32(x.y), lo_f32(x.z), hi_f32(x.z), lo_f32(x.w),
+                 hi_f32(x.w)}};
+    } else if constexpr (P == 4) {
+        const u32x2 x = load_as<kOnce, loose_u32x2>(p);
+        return {{lo_f32(x.x), hi_f32(x.x), lo_f32(x.y), hi_f32(x.y)}};
     } else {
-        for (int i = 0; i < 7; ++i)
-            if (i < count)
-                p[i] = e.v[i];
+        return {{h_f32(*p)}};
     }
 }
-
-// How many of the 8 elements from column c a row of dim elements has.
-__device__ __forceinline__ int columns_left(int64_t dim, int64_t c) {
-    return dim - c >= 8 ? 8 : dim > c ? int(dim - c) : 0;
+template <int P, bool kOnce = false>
+__device__ __forceinline__ Some<P> load_some(const float *p) {
+    Some<P> e;
+    if constexpr (P == 1)
+        e.v[0] = *p;
+    else
+        for (int i = 0; i < P; i += 4) {
+            const f32x4 x = load_as<kOnce, loose_f32x4>(p + i);
+            for (int k = 0; k < 4; ++k)
+                e.v[i + k] = x[k];
+        }
+    return e;
 }
+template <int P>
+__device__ __forceinline__ void store_some(uint16_t *p, const Some<P> &e) {
+    if constexpr (P == 8)
+        *reinterpret_cast<loose_u32x4 *>(p) = u32x4{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3]),
+                                                  to_bf16x2(e.v[4], e.v[5]), to_bf16x2(e.v[6], e.v[7])};
+    else if constexpr (P == 4)
+        *reinterpret_cast<loose_u32x2 *>(p) = u32x2{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3])};
+    else
+        *p = uint16_t(to_bf16x2(e.v[0], 0.0f));
+}
+template <int P>
+__device__ __forceinline__ void store_some(float *p, const Some<P> &e) {
+    if constexpr (P == 1)
+        *p = e.v[0];
+    else
+        for (int i = 0; i < P; i += 4)
+            *reinterpret_cast<loose_f32x4 *>(p + i) = f32x4{e.v[i], e.v[i + 1], e.v[i + 2], e.v[i + 3]};
+}
+
+template <int P>
+__device__ __forceinline__ void add(Some<P> &e, const Some<P> &x) {
+    for (int i = 0; i < P; ++i)
+        e.v[i] += x.v[i];
+}
+
+// The P columns, from `at`, that a lane takes of a row of dim >= P elements:
+// from c, or the row's last P for the lane whose own, from c, are fewer. The
+// first `skip` of those are the lane's before it as well, which writes the
+// same values.
+template <int P>
+struct Columns {
+    int64_t at;
+    int skip;
+    bool any;
+    __device__ __forceinline__ Columns(int64_t c, int64_t dim)
+        : at(c < dim - P ? c : dim - P), skip(c < dim ? int(c - at) : 0), any(c < dim) {}
+};
 
 // ---- lookup ------------------------------------------------------------------------------
-// A wave takes kLookupWide columns of a row, all its loads first.
-constexpr int kLookupChunks = 4, kLookupWide = 512 * kLookupChunks;
+// A wave takes kLookupChunks chunks of 64 lanes' columns of a row, all its
+// loads first.
+constexpr int kLookupChunks = 2;
 
-template <typename T>
+template <typename T, int P>
 __global__ __launch_bounds__(256) void lookup_kernel(LookupArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t c0 = int64_t(blockIdx.y) * kLookupWide + lane * 8;
+    const int64_t c0 = int64_t(blockIdx.y) * (64 * P * kLookupChunks) + lane * P;
     for (int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); i < a.n; i += int64_t(gridDim.x) * 4) {
         const int64_t token = a.tokens[i];
         T *out = static_cast<T *>(a.out) + i * a.stride;
         const bool named = token >= 0 && token < a.vocab;
         const uint16_t *row = a.w + (named ? token : 0) * a.dim;
-        Eight e[kLookupChunks];
+        Some<P> e[kLookupChunks];
 #pragma unroll
         for (int k = 0; k < kLookupChunks; ++k) {
-            const int64_t c = c0 + k * 512;
-            e[k] = named && c < a.dim ? read8(row + c, columns_left(a.dim, c)) : Eight{};
+            const Columns<P> c(c0 + k * 64 * P, a.dim);
+            e[k] = named && c.any ? load_some<P>(row + c.at) : Some<P>{};
         }
 #pragma unroll
         for (int k = 0; k < kLookupChunks; ++k) {
-            const int64_t c = c0 + k * 512;
-            if (c >= a.dim)
-                break;
+            const Columns<P> c(c0 + k * 64 * P, a.dim);
             if (named)
                 for (float &v : e[k].v)
                     v = a.scale * v;
-            write8(out + c, e[k], columns_left(a.dim, c));
+            if (c.any)
+                store_some(out + c.at, e[k]);
         }
     }
 }
@@ -123,41 +138,88 @@ __device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
     return token >= 0 && token < vocab ? uint32_t(token) : uint32_t(vocab);
 }
 
+// Zeros to [0, n) by 256 threads of each of the launch's workgroups from
+// `first` on; the first of those also writes the few elements before and behind
+// 16-byte alignment. Few writers are faster than many: 1 GB by 256 workgroups
+// in 160 us, by 512 in 195, by 4096 in 232, non-temporally in 166 to 264.
+struct ZeroArgs {
+    uint16_t *p;
+    int64_t n;
+    int32_t first;  // workgroups before it do something else
+};
+constexpr int kZeroThreads = 256, kZeroGroups = 256;
+
+__device__ __forceinline__ void fill_zero(const ZeroArgs &z) {
+    if (threadIdx.x >= kZeroThreads)
+        return;
+    const int64_t head = (16 - (reinterpret_cast<uintptr_t>(z.p) & 15)) % 16 / 2, from = head < z.n ? head : z.n;
+    const int64_t chunks = (z.n - from) / 8, upto = from + chunks * 8;
+    if (int(blockIdx.x) == z.first) {
+        if (int64_t(threadIdx.x) < from)
+            z.p[threadIdx.x] = 0;
+        if (upto + threadIdx.x < z.n)
+            z.p[upto + threadIdx.x] = 0;
+    }
+    u32x4 *q = reinterpret_cast<u32x4 *>(z.p + from);
+    const int64_t step = int64_t(gridDim.x - z.first) * kZeroThreads;
+    for (int64_t i = int64_t(blockIdx.x - z.first) * kZeroThreads + threadIdx.x; i < chunks; i += step)
+        q[i] = u32x4{0, 0, 0, 0};
+}
+
+__global__ __launch_bounds__(kZeroThreads) void zero_kernel(ZeroArgs z) { fill_zero(z); }
+
 // Few positions: a position's place is the number of keys below its own, or
-// equal and before it. A workgroup counts for 64 positions, its 16 waves each
-// over a sixteenth of the keys, which all of them hold in LDS.
+// equal and before it. A workgroup counts for 32 positions, a lane each, each
+// half of its 16 waves over a 32nd of the keys, which all of them hold in LDS.
+// The workgroups from z.first on clear the gradient meanwhile.
 __global__ __launch_bounds__(1024) void rank_kernel(const int64_t *tokens, int64_t vocab, int n, uint32_t *key_out,
-                                                   uint32_t *pos_out) {
+                                                   uint32_t *pos_out, ZeroArgs z) {
     __shared__ __align__(16) uint32_t keys[kRankMax];
-    __shared__ int below[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int padded = (n + 63) & ~63;
-    for (int j = threadIdx.x; j < padded; j += 1024)
-        keys[j] = j < n ? key_of(tokens[j], vocab) : 0xffffffffu;
+    __shared__ int below[32][33];
+    if (int(blockIdx.x) >= z.first) {
+        fill_zero(z);
+        return;
+    }
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int padded = (n + 31) & ~31;
+    {
+        // all of a thread's loads, then its stores
+        constexpr int kEach = kRankMax / 1024;
+        uint32_t key[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int j = k * 1024 + threadIdx.x;
+            key[k] = j < n ? key_of(tokens[j], vocab) : 0xffffffffu;
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (k * 1024 + int(threadIdx.x) < padded)
+                keys[k * 1024 + threadIdx.x] = key[k];
+    }
     __syncthreads();
-    const int i0 = blockIdx.x * 64, i = i0 + lane;
+    const int i0 = blockIdx.x * 32, i = i0 + lane;
     const uint32_t mine = keys[i];   // i < padded
     int count = 0;
-    const int blocks = padded / 64, from = blocks * wave / 16, to = blocks * (wave + 1) / 16;
+    const int blocks = padded / 32, from = blocks * part / 32, to = blocks * (part + 1) / 32;
     for (int b = from; b < to; ++b) {
-        if (b * 64 == i0) {
-            for (int j = 0; j < 64; ++j)
+        if (b * 32 == i0) {
+            for (int j = 0; j < 32; ++j)
                 count += keys[i0 + j] < mine || (keys[i0 + j] == mine && j < lane);
             continue;
         }
         // equal keys count where they come before: k <= mine is k < mine + 1
-        const uint32_t limit = mine + (b * 64 < i0 ? 1u : 0u);
-#pragma unroll 4
-        for (int j = 0; j < 64; j += 4) {
-            const u32x4 k = *reinterpret_cast<const u32x4 *>(&keys[b * 64 + j]);
+        const uint32_t limit = mine + (b * 32 < i0 ? 1u : 0u);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const u32x4 k = *reinterpret_cast<const u32x4 *>(&keys[b * 32 + j]);
             count += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
         }
     }
-    below[wave][lane] = count;
+    below[part][lane] = count;
     __syncthreads();
-    if (wave == 0 && i < n) {
+    if (part == 0 && i < n) {
         int place = 0;
-        for (int w = 0; w < 16; ++w)
+        for (int w = 0; w < 32; ++w)
             place += below[w][lane];
         key_out[place] = mine;
         pos_out[place] = uint32_t(i);
@@ -165,29 +227,34 @@ __global__ __launch_bounds__(1024) void rank_kernel(const int64_t *tokens, int64
 }
 
 // More positions: by digits from the lowest, each pass stable. A workgroup
-// takes kSortItems positions, each of its 4 waves a quarter of them in order.
+// takes `items` positions, each of its 4 waves a quarter of them in order.
 struct SortArgs {
     const int64_t *tokens;  // the first pass's keys
     int64_t vocab, n, blocks;
     const uint32_t *key, *pos;
     uint32_t *key_out, *pos_out;
-    uint32_t *hist;  // [bin][workgroup]: counts, then where a workgroup's first of that digit goes
-    int shift, bits;
+    uint32_t *hist;  // [bin][workgroup]: counts, then the sum of those before; and each bin's total
+    int items, shift, bits;
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, int64_t i) {
     return a.tokens ? key_of(a.tokens[i], a.vocab) : a.key[i];
 }
 
-__global__ __launch_bounds__(256) void sort_count_kernel(SortArgs a) {
+// The first pass's workgroups from z.first on clear the gradient.
+__global__ __launch_bounds__(256) void sort_count_kernel(SortArgs a, ZeroArgs z) {
     __shared__ uint32_t count[kSortBins];
     const int bins = 1 << a.bits;
-    for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    if (int(blockIdx.x) >= z.first) {
+        fill_zero(z);
+        return;
+    }
+    for (int64_t b = blockIdx.x; b < a.blocks; b += z.first) {
         for (int d = threadIdx.x; d < bins; d += 256)
             count[d] = 0;
         __syncthreads();
-        for (int j = threadIdx.x; j < kSortItems; j += 256) {
-            const int64_t i = b * kSortItems + j;
+        for (int j = threadIdx.x; j < a.items; j += 256) {
+            const int64_t i = b * a.items + j;
             if (i < a.n)
                 atomicAdd(&count[(sort_key(a, i) >> a.shift) & (bins - 1)], 1u);
         }
@@ -198,19 +265,43 @@ __global__ __launch_bounds__(256) void sort_count_kernel(SortArgs a) {
     }
 }
 
-// hist to the sum of all entries before each, by one workgroup.
-__global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t *hist, int64_t entries) {
-    __shared__ uint32_t wave_sum[16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t before = 0;
-    for (int64_t i0 = 0; i0 < entries; i0 += 4096) {
-        const int64_t i = i0 + threadIdx.x * 4;
-        uint32_t v[4], own = 0;
-        for (int k = 0; k < 4; ++k) {
-            v[k] = i + k < entries ? hist[i + k] : 0u;
-            own += v[k];
+// Each digit's counts to the sum of those before (a wave a digit), and their
+// total behind them all: hist[bins * blocks + digit].
+__global__ __launch_bounds__(256) void sort_scan_kernel(SortArgs a) {
+    const int lane = threadIdx.x & 63, digit = blockIdx.x * 4 + (threadIdx.x >> 6), bins = 1 << a.bits;
+    if (digit >= bins)
+        return;
+    uint32_t *row = a.hist + digit * a.blocks, before = 0;
+    for (int64_t i0 = 0; i0 < a.blocks; i0 += 128) {
+        const int64_t i = i0 + lane * 2;
+        const uint32_t x = i < a.blocks ? row[i] : 0u, y = i + 1 < a.blocks ? row[i + 1] : 0u;
+        uint32_t upto = x + y;
+        for (int s = 1; s < 64; s <<= 1) {
+            const uint32_t other = __shfl_up(upto, s);
+            if (lane >= s)
+                upto += other;
         }
-        uint32_t upto = own;
+        const uint32_t at = before + upto - x - y;
+        if (i < a.blocks)
+            row[i] = at;
+        if (i + 1 < a.blocks)
+            row[i + 1] = at + x;
+        before += __shfl(upto, 63);
+    }
+    if (lane == 0)
+        a.hist[bins * a.blocks + digit] = before;
+}
+
+__global__ __launch_bounds__(256) void sort_move_kernel(SortArgs a) {
+    __shared__ uint32_t next[4][kSortBins];
+    __shared__ uint32_t start[kSortBins], wave_sum[4];  // of each digit: where its first goes
+    const int bins = 1 << a.bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    {
+        // digits 2t and 2t + 1
+        const int d = threadIdx.x * 2;
+        const uint32_t x = d < bins ? a.hist[bins * a.blocks + d] : 0u;
+        const uint32_t y = d + 1 < bins ? a.hist[bins * a.blocks + d + 1] : 0u;
+        uint32_t upto = x + y;
         for (int s = 1; s < 64; s <<= 1) {
             const uint32_t other = __shfl_up(upto, s);
             if (lane >= s)
@@ -219,36 +310,24 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t *hist, int64_t
         if (lane == 63)
             wave_sum[wave] = upto;
         __syncthreads();
-        uint32_t at = before + upto - own, total = 0;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave)
-                at += wave_sum[w];
-            total += wave_sum[w];
-        }
-        for (int k = 0; k < 4; ++k) {
-            if (i + k < entries)
-                hist[i + k] = at;
-            at += v[k];
-        }
-        before += total;
-        __syncthreads();
+        uint32_t at = upto - x - y;
+        for (int w = 0; w < wave; ++w)
+            at += wave_sum[w];
+        start[d] = at;
+        start[d + 1] = at + x;
     }
-}
-
-__global__ __launch_bounds__(256) void sort_move_kernel(SortArgs a) {
-    __shared__ uint32_t next[4][kSortBins];
-    const int bins = 1 << a.bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // the loop's first barrier comes before start is read
     for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
         for (int d = threadIdx.x; d < 4 * bins; d += 256)
             next[d / bins][d % bins] = 0;
         __syncthreads();
-        const int64_t i0 = b * kSortItems + wave * (kSortItems / 4);
-        for (int j = lane; j < kSortItems / 4; j += 64)
+        const int64_t i0 = b * a.items + wave * (a.items / 4);
+        for (int j = lane; j < a.items / 4; j += 64)
             if (i0 + j < a.n)
                 atomicAdd(&next[wave][(sort_key(a, i0 + j) >> a.shift) & (bins - 1)], 1u);
         __syncthreads();
         for (int d = threadIdx.x; d < bins; d += 256) {
-            uint32_t at = a.hist[d * a.blocks + b];
+            uint32_t at = start[d] + a.hist[d * a.blocks + b];
             for (int w = 0; w < 4; ++w) {
                 const uint32_t c = next[w][d];
                 next[w][d] = at;
@@ -256,7 +335,7 @@ __global__ __launch_bounds__(256) void sort_move_kernel(SortArgs a) {
             }
         }
         __syncthreads();
-        for (int j = lane; j < kSortItems / 4; j += 64) {
+        for (int j = lane; j < a.items / 4; j += 64) {
             const int64_t i = i0 + j;
             const bool in = i < a.n;
             const uint32_t key = in ? sort_key(a, i) : 0u;
@@ -282,116 +361,145 @@ __global__ __launch_bounds__(256) void sort_move_kernel(SortArgs a) {
 }
 
 // ---- sums of rows ----------------------------------------------------------------------------
-
-// Adds the rows of positions pos[from, to) to e, in that order, loads ahead.
-template <typename T>
-__device__ __forceinline__ void add_rows(Eight &e, const T *x, int64_t stride, const uint32_t *pos, int64_t from,
-                                         int64_t to, int count) {
-    int64_t i = from;
-    for (; i + 8 <= to; i += 8) {
-        Eight r[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            r[k] = read8(x + int64_t(pos[i + k]) * stride, count);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            for (int c = 0; c < 8; ++c)
-                e.v[c] += r[k].v[c];
-    }
-    for (; i < to; ++i) {
-        const Eight r = read8(x + int64_t(pos[i]) * stride, count);
-        for (int c = 0; c < 8; ++c)
-            e.v[c] += r.v[c];
-    }
-}
-
+// A run is the sorted positions of one token. A wave sums a chunk of
+// consecutive positions at its lanes' columns, whatever runs they belong to, so that
+// the work is even however often a token occurs. A run within the chunk is
+// finished there; of a run that goes on in other chunks the chunk's part is
+// left in fp32, and join_kernel adds the parts in order.
 struct SumArgs {
     RowsArgs r;
     const uint32_t *key, *pos;  // sorted
-    float *partial;             // [chunk][dim]
-    int64_t chunks;             // 0: no partial sums
+    int32_t chunk;
+    int64_t chunks;
+    float *part;  // [chunk][2][dim]: of a run from before, of one that starts here and goes on
 };
 
-// The sum of every chunk that is all one token's.
-template <typename T>
-__global__ __launch_bounds__(64) void run_chunk_kernel(SumArgs a) {
-    const int64_t c = int64_t(blockIdx.y) * 512 + threadIdx.x * 8;
-    const int count = columns_left(a.r.dim, c);
-    for (int64_t b = blockIdx.x; b < a.chunks; b += gridDim.x) {
-        const int64_t from = b * kRunChunk;
-        const uint32_t key = a.key[from];
-        if (key == uint32_t(a.r.vocab) || a.key[from + kRunChunk - 1] != key || count <= 0)
-            continue;
-        Eight e{};
-        add_rows(e, static_cast<const T *>(a.r.x) + c, a.r.stride, a.pos, from, from + kRunChunk, count);
-        write8(a.partial + b * a.r.dim + c, e, count);
+template <bool kAdd, int P>
+__device__ __forceinline__ void write_row(const RowsArgs &r, uint32_t row, const Columns<P> &c, Some<P> e) {
+    uint16_t *out = r.g + int64_t(row) * r.dim + c.at;
+    for (float &v : e.v)
+        v = r.scale * v;
+    if constexpr (kAdd) {
+        if (c.skip == 0) {
+            const Some<P> old = load_some<P>(out);
+            for (int i = 0; i < P; ++i)
+                e.v[i] = old.v[i] + e.v[i];
+            store_some(out, e);
+        } else {
+            // another wave may be adding to the columns that are not this lane's own
+            for (int i = 1; i < P; ++i)
+                if (i >= c.skip)
+                    store_some(out + i, Some<1>{{h_f32(out[i]) + e.v[i]}});
+        }
+    } else {
+        store_some(out, e);
     }
 }
 
-// The first of key[from, to) that is not below `limit`: all 64 lanes probe.
-__device__ __forceinline__ int64_t first_not_below(const uint32_t *key, int64_t from, int64_t to, uint32_t limit) {
-    const int lane = threadIdx.x & 63;
-    while (from < to) {
-        const int64_t step = (to - from + 63) / 64, probe = from + (lane + 1) * step - 1;
-        const int below = __popcll(__ballot(probe < to && key[probe] < limit));
-        from += below * step;
-        to = to < from + step - 1 ? to : from + step - 1;
-    }
-    return to;
-}
-
-// A wave takes kRowGroup rows of the matrix at 512 columns.
-constexpr int kRowGroup = 16;
-
-template <typename T>
-__global__ __launch_bounds__(64) void rows_kernel(SumArgs a) {
+template <typename T, int P, bool kAdd>
+__global__ __launch_bounds__(256) void runs_kernel(SumArgs a) {
     const RowsArgs &r = a.r;
-    const int64_t c = int64_t(blockIdx.y) * 512 + threadIdx.x * 8;
-    const int count = columns_left(r.dim, c);
-    const int64_t groups = (r.vocab + kRowGroup - 1) / kRowGroup;
-    const T *x = static_cast<const T *>(r.x) + c;
-    for (int64_t b = blockIdx.x; b < groups; b += gridDim.x) {
-        const int64_t row0 = b * kRowGroup;
-        int64_t at = first_not_below(a.key, 0, r.n, uint32_t(row0));
-        for (int64_t row = row0; row < row0 + kRowGroup && row < r.vocab; ++row) {
-            // the row's positions [at, end)
-            const int64_t look = at + (threadIdx.x & 63);
-            const int named = __popcll(__ballot(look < r.n && a.key[look] == uint32_t(row)));
-            const int64_t end = named < 64 ? at + named : first_not_below(a.key, at + 64, r.n, uint32_t(row) + 1);
-            uint16_t *out = r.g + row * r.dim + c;
-            if (count > 0 && (end > at || !r.accumulate)) {
-                Eight e{};
-                const int64_t b0 = (at + kRunChunk - 1) / kRunChunk, b1 = end / kRunChunk;
-                if (a.chunks && b0 < b1) {
-                    add_rows(e, x, r.stride, a.pos, at, b0 * kRunChunk, count);
-                    for (int64_t k = b0; k < b1; ++k) {
-                        const Eight p = read8(a.partial + k * r.dim + c, count);
-                        for (int i = 0; i < 8; ++i)
-                            e.v[i] += p.v[i];
-                    }
-                    add_rows(e, x, r.stride, a.pos, b1 * kRunChunk, end, count);
-                } else {
-                    add_rows(e, x, r.stride, a.pos, at, end, count);
-                }
-                if (end > at)
-                    for (float &v : e.v)
-                        v = r.scale * v;
-                if (r.accumulate) {
-                    const Eight old = read8(out, count);
-                    for (int i = 0; i < 8; ++i)
-                        e.v[i] = old.v[i] + e.v[i];
-                }
-                write8(out, e, count);
+    const int lane = threadIdx.x & 63;
+    const Columns<P> c((int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * P, r.dim);
+    const T *x = static_cast<const T *>(r.x) + c.at;
+    const uint32_t none = uint32_t(r.vocab);
+    for (int64_t b = blockIdx.x; b < a.chunks; b += gridDim.x) {
+        const int64_t i0 = b * a.chunk;
+        const int in = r.n - i0 < a.chunk ? int(r.n - i0) : a.chunk;
+        const uint32_t my_key = lane < in ? a.key[i0 + lane] : none, my_pos = lane < in ? a.pos[i0 + lane] : 0u;
+        const uint32_t before = i0 > 0 ? a.key[i0 - 1] : none, after = i0 + in < r.n ? a.key[i0 + in] : none;
+        const int named = __popcll(__ballot(my_key != none));   // those without a row come last
+        Some<P> e{};
+        bool from_before = false;
+        for (int j0 = 0; j0 < named; j0 += 8) {
+            Some<P> v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int j = j0 + k < named ? j0 + k : named - 1;
+                v[k] = c.any ? load_some<P, true>(x + int64_t(__builtin_amdgcn_readlane(my_pos, j)) * r.stride) : Some<P>{};
             }
-            at = end;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int j = j0 + k;
+                if (j >= named)
+                    break;
+                const uint32_t key = __builtin_amdgcn_readlane(my_key, j);
+                if (j == 0)
+                    from_before = key == before;
+                add(e, v[k]);
+                const bool last = j == in - 1;
+                if ((last ? after : uint32_t(__builtin_amdgcn_readlane(my_key, last ? j : j + 1))) == key && !last)
+                    continue;
+                const bool goes_on = last && after == key;
+                if (c.any) {
+                    if (from_before || goes_on)
+                        store_some(a.part + (2 * b + !from_before) * r.dim + c.at, e);
+                    else
+                        write_row<kAdd>(r, key, c, e);
+                }
+                from_before = false;
+                e = Some<P>{};
+            }
         }
     }
 }
 
-__global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
-    const int64_t chunks = (n + 7) / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256)
-        write8(p + i * 8, Eight{}, columns_left(n, i * 8));
+// A run that starts in chunk b and goes on: its parts, a quarter by each of
+// the workgroup's waves, then the four.
+template <int P, bool kAdd>
+__global__ __launch_bounds__(256) void join_kernel(SumArgs a) {
+    __shared__ Some<P> red[3][64];
+    const RowsArgs &r = a.r;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Columns<P> c((int64_t(blockIdx.y) * 64 + lane) * P, r.dim);
+    for (int64_t b = blockIdx.x; b + 1 < a.chunks; b += gridDim.x) {
+        const int64_t next = (b + 1) * a.chunk;
+        const uint32_t key = a.key[next - 1];
+        if (key == uint32_t(r.vocab) || a.key[next] != key || (a.key[b * a.chunk] == key && b > 0 && a.key[b * a.chunk - 1] == key))
+            continue;
+        // chunks b + 1 .. b + whole are all this run's, and one more begins with it
+        // unless the run ends with them
+        int64_t whole = 0;
+        for (;;) {
+            const int64_t last = (b + 2 + whole + lane) * a.chunk - 1;
+            const uint64_t other = ~__ballot(last < r.n && a.key[last] == key);
+            if (other) {
+                whole += __builtin_ctzll(other);
+                break;
+            }
+            whole += 64;
+        }
+        const int64_t begin = (b + 1 + whole) * a.chunk;
+        const int64_t parts = whole + (begin < r.n && a.key[begin] == key);   // of chunks b + 1, b + 2, ...
+        Some<P> e{};
+        if (c.any) {
+            if (wave == 0)
+                e = load_some<P, true>(a.part + (2 * b + 1) * r.dim + c.at);
+            const float *part = a.part + 2 * (b + 1) * r.dim + c.at;
+            const int64_t to = parts * (wave + 1) / 4;
+            int64_t k = parts * wave / 4;
+            for (; k + 8 <= to; k += 8) {
+                Some<P> v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = load_some<P, true>(part + 2 * (k + u) * r.dim);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    add(e, v[u]);
+            }
+            for (; k < to; ++k)
+                add(e, load_some<P, true>(part + 2 * k * r.dim));
+        }
+        if (wave > 0)
+            red[wave - 1][lane] = e;
+        __syncthreads();
+        if (wave == 0 && c.any) {
+            for (int w = 0; w < 3; ++w)
+                add(e, red[w][lane]);
+            write_row<kAdd>(r, key, c, e);
+        }
+        __syncthreads();
+    }
 }
 
 // ---- around the cross entropy's products --------------------------------------------------------
@@ -402,8 +510,15 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t
     const int64_t per = kdim / 8;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / per, c = i % per * 8;
-        const int count = columns_left(dim, c);
-        write8(to + r * kdim + c, count > 0 ? read8(from + r * stride + c, count) : Eight{}, 8);
+        const uint16_t *p = from + r * stride + c;
+        u32x4 x = {0, 0, 0, 0};
+        if (c + 8 <= dim)
+            x = *reinterpret_cast<const loose_u32x4 *>(p);
+        else
+            for (int k = 0; k < 7; ++k)
+                if (c + k < dim)
+                    x[k >> 1] |= uint32_t(p[k]) << (k & 1) * 16;
+        *reinterpret_cast<u32x4 *>(to + r * kdim + c) = x;
     }
 }
 
@@ -424,14 +539,14 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t *from, in
         }
 #pragma unroll
         for (int h = 0; h < 16; h += 8) {
-            const int count = keep ? columns_left(dim, c0 + part + h) : 0;
+            const int64_t left = keep ? dim - (c0 + part + h) : 0;
             u32x4 x = {0, 0, 0, 0};
             const uint16_t *p = from + (r0 + r) * stride + c0 + part + h;
-            if (count >= 8)
-                x = reinterpret_cast<const Loose16 *>(p)->v;
+            if (left >= 8)
+                x = *reinterpret_cast<const loose_u32x4 *>(p);
             else
                 for (int i = 0; i < 7; ++i)
-                    if (i < count)
+                    if (i < left)
                         x[i >> 1] |= uint32_t(p[i]) << (i & 1) * 16;
             for (int i = 0; i < 8; ++i)
                 tile[r][part + h + i] = uint16_t(x[i >> 1] >> (i & 1) * 16);
@@ -481,27 +596,27 @@ __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *pa
 }
 
 // The splits' sums of grad_hidden, added in their order and rounded.
-template <typename T>
+template <typename T, int P>
 __global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum, int64_t splits, int64_t kdim) {
-    const int64_t per = kdim / 8;
+    const int64_t per = (a.dim + P - 1) / P;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.n * per; i += int64_t(gridDim.x) * 256) {
-        const int64_t r = i / per, c = i % per * 8;
-        const int count = columns_left(a.dim, c);
-        if (count <= 0)
-            continue;
+        const int64_t r = i / per;
+        const Columns<P> c(i % per * P, a.dim);
         const int64_t target = a.targets[r];
-        Eight e{};
+        Some<P> e{};
         if (target >= 0 && target < a.vocab)
-            for (int64_t s = 0; s < splits; ++s) {
-                const Eight x = read8(sum + (s * a.n + r) * kdim + c, 8);
-                for (int k = 0; k < 8; ++k)
-                    e.v[k] += x.v[k];
-            }
-        write8(static_cast<T *>(a.grad_hidden) + r * a.grad_hidden_stride + c, e, count);
+            for (int64_t s = 0; s < splits; ++s)
+                add(e, load_some<P, true>(sum + (s * a.n + r) * kdim + c.at));
+        store_some(static_cast<T *>(a.grad_hidden) + r * a.grad_hidden_stride + c.at, e);
     }
 }
 
 unsigned grid_of(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, std::min<int64_t>(kMaxGrid, 1 << 20))); }
+
+// Workgroups that clear n elements.
+unsigned zero_grid(int64_t n) {
+    return unsigned(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 8 * kZeroThreads), grid_of(kZeroGroups))));
+}
 
 // W and hidden as the products need them: in place where their rows are 16-byte
 // aligned whole steps, else a copy.
@@ -544,36 +659,47 @@ const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, const Operands &o, 
 
 hipError_t launch_zero(uint16_t *p, int64_t n, hipStream_t stream) {
     if (n > 0)
-        zero_kernel<<<grid_of(ceil_div(n, 2048)), 256, 0, stream>>>(p, n);
+        zero_kernel<<<zero_grid(n), kZeroThreads, 0, stream>>>(ZeroArgs{p, n, 0});
     return hipGetLastError();
 }
 
 hipError_t launch_lookup(const LookupArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return hipSuccess;
-    const dim3 grid(grid_of(ceil_div(a.n, 4)), unsigned(ceil_div(a.dim, kLookupWide)));
+    const int P = a.dim >= 8 ? 8 : 1;
+    const dim3 grid(grid_of(ceil_div(a.n, 4)), unsigned(ceil_div(a.dim, 64 * P * kLookupChunks)));
+    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a); };
     if (a.f32)
-        lookup_kernel<float><<<grid, 256, 0, stream>>>(a);
+        P == 8 ? go(lookup_kernel<float, 8>) : go(lookup_kernel<float, 1>);
     else
-        lookup_kernel<uint16_t><<<grid, 256, 0, stream>>>(a);
+        P == 8 ? go(lookup_kernel<uint16_t, 8>) : go(lookup_kernel<uint16_t, 1>);
     return hipGetLastError();
 }
 
+// The sums of rows, P columns a lane.
+template <typename T, int P, bool kAdd>
+void launch_sums(const SumArgs &s, hipStream_t stream) {
+    const int64_t waves = std::min<int64_t>(4, ceil_div(s.r.dim, 64 * P));
+    const unsigned chunks = grid_of(s.chunks);
+    runs_kernel<T, P, kAdd><<<dim3(chunks, unsigned(ceil_div(s.r.dim, 64 * P * waves))), unsigned(64 * waves), 0, stream>>>(s);
+    if (s.chunks > 1) {
+        constexpr int J = P == 1 ? 1 : 4;   // of fp32
+        join_kernel<J, kAdd><<<dim3(chunks, unsigned(ceil_div(s.r.dim, 64 * J))), 256, 0, stream>>>(s);
+    }
+}
+
 hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
-    if (!a.accumulate)
-        if (hipError_t e = launch_zero(a.g + a.vocab * a.dim, a.numel - a.vocab * a.dim, stream); e != hipSuccess)
-            return e;
     if (a.n == 0)
-        return a.accumulate ? hipSuccess : launch_zero(a.g, a.vocab * a.dim, stream);
+        return a.accumulate ? hipSuccess : launch_zero(a.g, a.numel, stream);
     const RowsLayout l = rows_layout(a.n, a.dim);
     char *ws = static_cast<char *>(a.workspace);
     auto u32 = [&](int64_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
-    SumArgs s{};
-    s.r = a;
     int set = 0;
     if (a.n <= kRankMax) {
-        rank_kernel<<<unsigned(ceil_div(a.n, 64)), 1024, 0, stream>>>(a.tokens, a.vocab, int(a.n), u32(l.key[0]),
-                                                                     u32(l.pos[0]));
+        const unsigned blocks = unsigned(ceil_div(a.n, 32));
+        const ZeroArgs z{a.g, a.numel, int32_t(blocks)};
+        rank_kernel<<<blocks + (a.accumulate ? 0 : zero_grid(a.numel)), 1024, 0, stream>>>(
+            a.tokens, a.vocab, int(a.n), u32(l.key[0]), u32(l.pos[0]), z);
     } else {
         const int bits = 64 - __builtin_clzll(uint64_t(a.vocab)), passes = (bits + 8) / 9;
         const int digit = (bits + passes - 1) / passes;
@@ -582,6 +708,7 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
         p.n = a.n;
         p.blocks = l.blocks;
         p.hist = u32(l.hist);
+        p.items = l.items;
         p.bits = digit;
         for (int k = 0; k < passes; ++k) {
             p.tokens = k ? nullptr : a.tokens;
@@ -591,28 +718,27 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
             p.key_out = u32(l.key[set]);
             p.pos_out = u32(l.pos[set]);
             p.shift = k * digit;
-            sort_count_kernel<<<grid_of(l.blocks), 256, 0, stream>>>(p);
-            sort_scan_kernel<<<1, 1024, 0, stream>>>(p.hist, l.blocks << digit);
+            const unsigned count = grid_of(l.blocks);
+            sort_count_kernel<<<count + (k || a.accumulate ? 0 : zero_grid(a.numel)), 256, 0, stream>>>(
+                p, ZeroArgs{a.g, a.numel, int32_t(count)});
+            sort_scan_kernel<<<unsigned(ceil_div(int64_t(1) << digit, 4)), 256, 0, stream>>>(p);
             sort_move_kernel<<<grid_of(l.blocks), 256, 0, stream>>>(p);
         }
     }
+    SumArgs s{};
+    s.r = a;
     s.key = u32(l.key[set]);
     s.pos = u32(l.pos[set]);
-    s.partial = reinterpret_cast<float *>(ws + l.partial);
+    s.chunk = l.chunk;
     s.chunks = l.chunks;
-    const unsigned across = unsigned(ceil_div(a.dim, 512));
-    if (s.chunks) {
-        const dim3 grid(grid_of(s.chunks), across);
-        if (a.f32)
-            run_chunk_kernel<float><<<grid, 64, 0, stream>>>(s);
-        else
-            run_chunk_kernel<uint16_t><<<grid, 64, 0, stream>>>(s);
-    }
-    const dim3 grid(grid_of(ceil_div(a.vocab, kRowGroup)), across);
-    if (a.f32)
-        rows_kernel<float><<<grid, 64, 0, stream>>>(s);
+    s.part = reinterpret_cast<float *>(ws + l.part);
+    auto go = [&](auto f32, auto bf16) { (a.f32 ? f32 : bf16)(s, stream); };
+    if (a.accumulate)
+        a.dim >= 8 ? go(launch_sums<float, 4, true>, launch_sums<uint16_t, 8, true>)
+                   : go(launch_sums<float, 1, true>, launch_sums<uint16_t, 1, true>);
     else
-        rows_kernel<uint16_t><<<grid, 64, 0, stream>>>(s);
+        a.dim >= 8 ? go(launch_sums<float, 4, false>, launch_sums<uint16_t, 8, false>)
+                   : go(launch_sums<float, 1, false>, launch_sums<uint16_t, 1, false>);
     return hipGetLastError();
 }
 
@@ -720,10 +846,11 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     }
     if (a.grad_hidden) {
         const unsigned grid = grid_of(ceil_div(a.n * l.kdim, 2048));
+        auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a, sum, l.splits, l.kdim); };
         if (a.f32)
-            hidden_kernel<float><<<grid, 256, 0, stream>>>(a, sum, l.splits, l.kdim);
+            a.dim >= 8 ? go(hidden_kernel<float, 8>) : go(hidden_kernel<float, 1>);
         else
-            hidden_kernel<uint16_t><<<grid, 256, 0, stream>>>(a, sum, l.splits, l.kdim);
+            a.dim >= 8 ? go(hidden_kernel<uint16_t, 8>) : go(hidden_kernel<uint16_t, 1>);
     }
     return hipGetLastError();
 }
