@@ -12,7 +12,7 @@
 namespace zdo {
 
 constexpr int64_t kVocabMaxN = int64_t(1) << 30;
-constexpr int64_t kCeMaxN = int64_t(1) << 22;  // rows of d^T: 256 of them within 32 bits of bytes
+constexpr int64_t kCeMaxN = int64_t(1) << 22;  // so that tiles are numbered in 32 bits
 constexpr int64_t kVocabMaxRows = int64_t(1) << 30;
 constexpr int64_t kVocabMaxDim = int64_t(1) << 20;
 constexpr int64_t kVocabMaxStride = int64_t(1) << 30;
@@ -94,8 +94,13 @@ inline RowsLayout rows_layout(int64_t n, int64_t dim) {
 // ---- cross entropy -----------------------------------------------------------------
 
 // C[m][n] = sum over k of A[m][k] B[n][k], in tiles (vocab_gemm.hip). A and B
-// are bf16 rows, 16-byte aligned, strides of a multiple of 8 elements, K a
-// multiple of kDepth. What becomes of C is the epilogue's.
+// are bf16, rows of k (long) or, for each k, a row of m or n (wide), 16-byte
+// aligned, strides of a multiple of 8 elements; long rows have a multiple of
+// kDepth elements, wide ones at least m or n up to a multiple of 8. Which is
+// which, and what becomes of C, is the epilogue's:
+//   kScore, kDiff: A and B long; kSum: A wide, B long (k of it up to a multiple
+//   of kDepth: zeros); kRows: A wide (with zero rows from k on, up to a multiple
+//   of kDepth), B wide (finite ones).
 constexpr int kDepth = 64;
 
 enum Epilogue : int { kScore, kDiff, kSum, kRows };
@@ -115,11 +120,10 @@ struct GemmArgs {
     float2 *part;
     int64_t tile0;  // the piece's first tile
     float *pick;
-    // kDiff: d in both orders, zero up to the next multiple of kDepth of the
-    // other index
+    // kDiff: d, [n][m], zero up to the next multiple of kDepth of both
     const float *lse, *weight;
-    uint16_t *d, *dt;
-    int64_t ldd, lddt;
+    uint16_t *d;
+    int64_t ldd;
 
     // kSum: fp32 [split][n][lds], added to what is there unless `first`
     float *sum;
@@ -140,15 +144,17 @@ inline bool wide_tiles(int64_t m, int64_t n, int64_t splits) {
 }
 inline int64_t tile_rows(int64_t m, int64_t n) { return wide_tiles(m, n, 1) ? 256 : kTileRowsMin; }
 
-// A call's workspace. The vocabulary is taken in pieces of `piece` rows.
-// (elements of d in one order: at most 2^26, 128 MB, so that both orders stay
-// in the 256 MB Infinity Cache between the product that writes them and the
-// two that read them, but at least 256 rows; of the piece's copies of W: at
-// most 2^27).
+#ifndef ZP
+#define ZP 27
+#endif
+// A call's workspace. The vocabulary is taken in pieces of `piece` rows: at most
+// 2^27 elements of d (256 MB, the size of the Infinity Cache that they go
+// through to the two products that read them), but at least 256 rows, and at
+// most 2^27 elements of a copy of W.
 struct CeLayout {
     int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
     int64_t splits;                   // of grad_hidden's sum
-    int64_t hidden, hidden_t, w, w_t, d, d_t, sum, part, pick, bytes;
+    int64_t hidden, w, d, sum, part, pick, bytes;
 };
 
 // Splits of the sum over the vocabulary that grad_hidden is: as many as give
@@ -163,7 +169,7 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     CeLayout l{};
     l.kdim = round_up(dim, kDepth);
     l.npad = round_up(std::max<int64_t>(n, 1), kDepth);
-    int64_t most = std::min((int64_t(1) << 26) / l.npad, (int64_t(1) << 27) / l.kdim);
+    int64_t most = std::min((int64_t(1) << ZP) / l.npad, (int64_t(1) << 27) / l.kdim);
     most = std::max<int64_t>(256, most / 256 * 256);
     const int64_t pieces = ceil_div(vocab, most);
     l.piece = std::min(vocab, round_up(ceil_div(vocab, pieces), 256));
@@ -175,7 +181,7 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
         at += round_up(bytes, 256);
         return here;
     };
-    l.hidden = take(2 * n * l.kdim);
+    l.hidden = take(2 * l.npad * l.kdim);
     l.w = take(2 * l.piece * l.kdim);
     const int64_t both = at;
     // the loss
@@ -184,10 +190,7 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     const int64_t loss = at;
     // its gradient
     at = both;
-    l.hidden_t = take(2 * dim * l.npad);
-    l.w_t = take(2 * dim * l.vpad);
-    l.d = take(2 * n * l.vpad);
-    l.d_t = take(2 * l.piece * l.npad);
+    l.d = take(2 * l.npad * l.vpad);
     l.sum = take(4 * l.splits * n * l.kdim);
     l.bytes = std::max<int64_t>(std::max(at, loss), 256);
     return l;

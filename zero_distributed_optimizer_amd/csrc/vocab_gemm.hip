@@ -2,11 +2,18 @@
 // for gfx950: the logits of a piece of the vocabulary with the softmax's
 // statistics or its gradient as epilogue, and the two gradients' products.
 //
-// One kernel: C[m][n] = sum over k of A[m][k] B[n][k], both operands with k
-// contiguous, on v_mfma_f32_16x16x32_bf16. A workgroup takes a tile of C; it
-// stages kDepth columns of both operands at a time in LDS, straight from
-// memory (16 bytes a lane), one step ahead of the products.
+// One kernel: C[m][n] = sum over k of A[m][k] B[n][k] on
+// v_mfma_f32_16x16x32_bf16. An operand lies in memory either "long", rows of k
+// (W and hidden for the logits), or "wide", rows of m or n, one for each k (W
+// for grad_hidden, hidden and d for W's gradient): gfx950's transposing LDS
+// read gives the instruction its 8 consecutive k of a lane from either, so that
+// no product needs a transposed copy. A workgroup takes a tile of C and steps
+// over k by kStep; a step's part of both operands comes to LDS straight from
+// memory (16 bytes a lane), kSlots steps ahead, and from there to registers one
+// step ahead of the products.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "device.h"
 #include "vocab.h"
@@ -17,6 +24,7 @@ namespace zdo {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // 8 or 16 bytes at any address that is aligned to an element.
 template <typename V>
@@ -24,32 +32,157 @@ struct __attribute__((packed, aligned(2))) Loose {
     V v;
 };
 
-__device__ __forceinline__ void copy16_to_lds(const char *base, uint32_t offset, uint16_t *to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(base + offset),
-                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+// 16 bytes a lane from base + its offset to LDS, lane after lane from `to` (the
+// same for the whole wave) on. Written as an instruction, because the compiler
+// would wait for all such copies before every LDS read (it cannot tell the slots
+// apart); the waits are wait_and_meet's. It has no result in registers, and
+// nothing else here uses m0.
+__device__ __forceinline__ void copy16_to_lds(const char *base, uint32_t offset, const uint16_t *to) {
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint16_t *)to)));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
 }
 
 // exp(x - top) that is 1 at the top, whatever the top is (both infinite: the
 // difference would be NaN).
 __device__ __forceinline__ float exp_below(float x, float top) { return x == top ? 1.0f : __expf(x - top); }
 
+constexpr int kStep = 32, kSlots = 4;
+
+// One operand's part of a step in LDS, R rows or columns of C.
+//
+// Long: R rows of kStep elements (64 bytes). The 16-byte chunk c of row r lies at
+// c ^ spread(r), so that the rows that a fragment's read takes at one chunk are
+// in different banks, 8 or 16 of them at a time. The read gives lane l the 8
+// elements of k from (l / 16) * 8 of row l % 16.
+//
+// Wide: kStep rows of R elements. A transposing read takes, in each 16 lanes, 4
+// rows of 16 elements, a row's four 8-byte parts from 4 lanes, and gives lane i
+// the 4 rows' element i; two of them are a fragment. The 32-byte unit u of row r
+// lies at u ^ spread(r), so that the 8 rows that 32 lanes read are in different
+// banks.
+template <int R, int kWaves, bool kWide>
+struct Operand {
+    static constexpr int kLoads = R * kStep * 2 / 1024 / kWaves;  // of 1 KB, a wave
+    static constexpr int kRowBytes = kWide ? R * 2 : kStep * 2, kChunks = kRowBytes / 16;
+    const char *base;
+    uint32_t off[kLoads];
+    int64_t step;   // bytes from one step's part to the next
+    uint32_t ld2;   // bytes from row to row
+    int left;       // wide: rows of k that there are from base on
+    int lane, load0, last_chunk;
+
+    static __device__ __forceinline__ int spread(int r) {
+        return kWide ? (r & 3) | ((r >> 3) & 1) << 2 : ((r >> 1) & 3) ^ ((r >> 3) & 1);
+    }
+    __device__ __forceinline__ int row_of(int i) const { return (load0 + i) * (64 / kChunks) + lane / kChunks; }
+    // The chunk of its row that lane's 16 bytes of load i come from.
+    __device__ __forceinline__ int chunk_of(int i) const {
+        const int r = row_of(i), p = lane % kChunks;
+        if constexpr (kWide) {
+            const int c = ((p >> 1) ^ spread(r)) * 2 + (p & 1);
+            return c < last_chunk ? c : last_chunk;
+        } else {
+            return p ^ spread(r);
+        }
+    }
+
+    // Rows or columns [x0, x0 + R) of `count`, k from k0 on of `have`. What lies
+    // behind the last is read as the last: it is not kept (m and n), or meets
+    // zeros of the other operand (k).
+    __device__ __forceinline__ void start(const uint16_t *p, int64_t ld, int64_t x0, int64_t count, int64_t k0,
+                                          int64_t have, int wave, int l) {
+        lane = l;
+        load0 = wave * kLoads;
+        ld2 = uint32_t(ld * 2);
+        if constexpr (kWide) {
+            base = reinterpret_cast<const char *>(p + k0 * ld + x0);
+            step = ld * 2 * kStep;
+            left = int(have - k0 < (1 << 30) ? have - k0 : 1 << 30);
+            const int64_t chunks = (count - x0 + 7) / 8;   // rows are padded to 8 elements
+            last_chunk = chunks < kChunks ? int(chunks) - 1 : kChunks - 1;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                off[i] = uint32_t(row_of(i)) * ld2 + uint32_t(chunk_of(i)) * 16;
+        } else {
+            base = reinterpret_cast<const char *>(p + x0 * ld + k0);
+            step = kStep * 2;
+            const int last = int(count - x0 < R ? count - x0 : R) - 1;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = row_of(i);
+                off[i] = uint32_t(r < last ? r : last) * ld2 + uint32_t(chunk_of(i)) * 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(uint16_t *stage) {
+        if (kWide && left < kStep) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = row_of(i);
+                off[i] = uint32_t(r < left ? r : left - 1) * ld2 + uint32_t(chunk_of(i)) * 16;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            copy16_to_lds(base, off[i], stage + (load0 + i) * 512);
+        base += step;
+        if (kWide)
+            left -= kStep;
+    }
+};
+
+// A wave's fragments of an operand: T of 16 rows or columns from x.
+template <int R, int T, bool kWide>
+struct Fragments {
+    int at[kWide ? T : 1];
+
+    __device__ __forceinline__ Fragments(int x, int lane) {
+        if constexpr (kWide) {
+            const int r = (lane >> 4) * 8 + ((lane & 15) >> 2), spread = Operand<R, 1, true>::spread(r);
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+                at[i] = r * R + (((x >> 4) + i) ^ spread) * 16 + (lane & 3) * 4;
+        } else {
+            at[0] = (x + (lane & 15)) * kStep + ((lane >> 4) ^ Operand<R, 1, false>::spread(lane & 15)) * 8;
+        }
+    }
+    __device__ __forceinline__ bf16x8 read(const uint16_t *slot, int i) const {
+        if constexpr (kWide) {
+            const bf16x4 lo = transposed(slot + at[i]), hi = transposed(slot + at[i] + 4 * R);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *reinterpret_cast<const bf16x8 *>(slot + at[0] + i * 16 * kStep);
+        }
+    }
+    static __device__ __forceinline__ bf16x4 transposed(const uint16_t *p) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4 *)p);
+    }
+};
+
+// Waits until at most `kLeft` of this wave's copies to LDS are still on their
+// way, then for the other waves to get here.
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+
 template <int BM, int BN, int WM, int WN, int E>
 __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WM * WN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles a wave
-    constexpr int RA = BM / 8 / kWaves, RB = BN / 8 / kWaves;  // loads of 8 rows a wave
-    // A step's rows of kDepth elements (128 bytes), A's then B's. The 16-byte
-    // chunk c of row r lies at c ^ (r & 7), so that the 16 rows that a
-    // fragment read takes at one chunk lie in different banks.
-    __shared__ __align__(1024) uint16_t stage[2][(BM + BN) * kDepth];
+    constexpr bool kWideA = E == kSum || E == kRows, kWideB = E == kRows;
+    __shared__ __align__(1024) uint16_t stage[kSlots][(BM + BN) * kStep];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / WN, wn = wave % WN;
     const int tiles_m = int((g.m + BM - 1) / BM), tiles_n = int((g.n + BN - 1) / BN);
     const int tiles = tiles_m * tiles_n * g.splits;
-    const int read_a = (wm * (BM / WM) + (lane & 15)) * kDepth;
-    const int read_b = (BM + wn * (BN / WN) + (lane & 15)) * kDepth;
-    const int chunk[2] = {((lane >> 4) ^ (lane & 7)) * 8, ((4 + (lane >> 4)) ^ (lane & 7)) * 8};
+    const Fragments<BM, TM, kWideA> frag_a(wm * (BM / WM), lane);
+    const Fragments<BN, TN, kWideB> frag_b(wn * (BN / WN), lane);
 
     for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
         // The tiles of an XCD (workgroups go to the 8 of them in turn) follow
@@ -62,35 +195,14 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
         const int tm = band * 8 + (t - band * 8 * tiles_n) % wide, tn = (t - band * 8 * tiles_n) / wide;
         const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
 
-        const int steps_all = int(g.k / kDepth);
+        const int steps_all = int((g.k + kStep - 1) / kStep);
         const int first = int(int64_t(steps_all) * split / g.splits);
         const int steps = int(int64_t(steps_all) * (split + 1) / g.splits) - first;
 
-        // rows behind the last are read as the last: what they give is not kept
-        uint32_t off_a[RA], off_b[RB];
-        const int last_a = int(g.m - m0 < BM ? g.m - m0 : BM) - 1, last_b = int(g.n - n0 < BN ? g.n - n0 : BN) - 1;
-#pragma unroll
-        for (int i = 0; i < RA; ++i) {
-            const int r = (wave * RA + i) * 8 + (lane >> 3);
-            off_a[i] = uint32_t(r < last_a ? r : last_a) * uint32_t(g.lda * 2) + uint32_t((lane & 7) ^ (lane >> 3)) * 16;
-        }
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int r = (wave * RB + i) * 8 + (lane >> 3);
-            off_b[i] = uint32_t(r < last_b ? r : last_b) * uint32_t(g.ldb * 2) + uint32_t((lane & 7) ^ (lane >> 3)) * 16;
-        }
-        const char *pa = reinterpret_cast<const char *>(g.a + m0 * g.lda + int64_t(first) * kDepth);
-        const char *pb = reinterpret_cast<const char *>(g.b + n0 * g.ldb + int64_t(first) * kDepth);
-        auto load = [&](int s) {
-#pragma unroll
-            for (int i = 0; i < RA; ++i)
-                copy16_to_lds(pa, off_a[i], &stage[s][(wave * RA + i) * 8 * kDepth]);
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-                copy16_to_lds(pb, off_b[i], &stage[s][(BM + (wave * RB + i) * 8) * kDepth]);
-            pa += kDepth * 2;
-            pb += kDepth * 2;
-        };
+        Operand<BM, kWaves, kWideA> a;
+        Operand<BN, kWaves, kWideB> b;
+        a.start(g.a, g.lda, m0, g.m, int64_t(first) * kStep, g.k, wave, lane);
+        b.start(g.b, g.ldb, n0, g.n, int64_t(first) * kStep, g.k, wave, lane);
 
         f32x4 acc[TM][TN];
 #pragma unroll
@@ -99,35 +211,76 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             for (int j = 0; j < TN; ++j)
                 acc[i][j] = f32x4{0, 0, 0, 0};
 
-        __syncthreads();   // the LDS is free
-        if (steps > 0)
-            load(0);
-        __syncthreads();
-        for (int k = 0; k < steps; ++k) {
-            const uint16_t *in = stage[k & 1];
-            if (k + 1 < steps)
-                load((k + 1) & 1);
+        constexpr int kCopies = a.kLoads + b.kLoads;   // a wave's, of a step
+        auto copy = [&](int slot) {
+            a.load(stage[slot]);
+            b.load(stage[slot] + BM * kStep);
+        };
+        bf16x8 fa[TM], fb[2][TN];
+        // Step k, whose fragments are in registers: its products, and meanwhile
+        // step k + 3's copies and, where an A fragment has been used, step k +
+        // 1's. Step k + 3 goes where step k - 1 was, whose fragments every wave
+        // has had in registers before it got here.
+        auto products = [&](int k, auto set, auto all) {
+            constexpr int kSet = decltype(set)::value;
+            constexpr bool kAll = decltype(all)::value;   // steps k + 1 to k + 3 exist
+            if (kAll || k + 2 < steps)
+                wait_and_meet<kCopies>();
+            else
+                wait_and_meet<0>();
+            if (kAll || k + 3 < steps)
+                copy((k + 3) % kSlots);
+            // (behind the last step: whatever the slot holds, unused)
+            const uint16_t *next = stage[(k + 1) % kSlots];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                bf16x8 a[TM], b[TN];
+            for (int i = 0; i < TM; ++i) {
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    a[i] = *reinterpret_cast<const bf16x8 *>(&in[read_a + i * 16 * kDepth + chunk[half]]);
+                for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j)
+                    fb[kSet ^ 1][j] = frag_b.read(next + BM * kStep, j);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    b[j] = *reinterpret_cast<const bf16x8 *>(&in[read_b + j * 16 * kDepth + chunk[half]]);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[kSet][j], acc[i][j], 0, 0, 0);
+                fa[i] = frag_a.read(next, i);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __syncthreads();   // the next step's loads have come, and this step's reads are done
+        };
+        __syncthreads();   // the LDS is free
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+            if (s < steps)
+                copy(s);
+        if (steps >= 3)
+            wait_and_meet<2 * kCopies>();
+        else
+            wait_and_meet<0>();
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[i] = frag_a.read(stage[0], i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[0][j] = frag_b.read(stage[0] + BM * kStep, j);
+        constexpr std::integral_constant<int, 0> even;
+        constexpr std::integral_constant<int, 1> odd;
+        int k = 0;
+        for (; k + 4 < steps; k += 2) {
+            products(k, even, std::true_type());
+            products(k + 1, odd, std::true_type());
         }
+        for (; k < steps; k += 2) {
+            products(k, even, std::false_type());
+            if (k + 1 < steps)
+                products(k + 1, odd, std::false_type());
+        }
+        __syncthreads();   // LDS serves the epilogue
 
         // acc[i][j][r] is C[m][n] with, from the tile's corner,
         //   m = wm * BM / WM + i * 16 + (lane / 16) * 4 + r, n = wn * BN / WN + j * 16 + lane % 16
-        const int wave_m = wm * (BM / WM), wave_n = wn * (BN / WN), lane_m = (lane >> 4) * 4, lane_n = lane & 15;
+        // (as numbers that the compiler does not know from before: it would
+        // compute the epilogue's addresses ahead of the tiles and spill them)
+        int epi_lane = lane, epi_wave = wave;
+        asm volatile("" : "+v"(epi_lane), "+s"(epi_wave));
+        const int wave_m = epi_wave / WN * (BM / WM), wave_n = epi_wave % WN * (BN / WN);
+        const int lane_m = (epi_lane >> 4) * 4, lane_n = epi_lane & 15;
         const int rows_in = int(g.m - m0 < BM ? g.m - m0 : BM), cols_in = int(g.n - n0 < BN ? g.n - n0 : BN);
 
         if constexpr (E == kScore) {
@@ -161,11 +314,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                             sum += exp_below(acc[i][j][r], top);
                 sum += __shfl_xor(sum, 16);
                 sum += __shfl_xor(sum, 32);
-                if (lane < 16)
-                    red[wm * BN + n] = {top, sum};
+                if (epi_lane < 16)
+                    red[epi_wave / WN * BN + n] = {top, sum};
             }
             __syncthreads();
-            const int n = threadIdx.x;
+            const int n = epi_wave * 64 + epi_lane;
             if (n < cols_in) {
                 float2 all = red[n];
 #pragma unroll
@@ -177,9 +330,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                 g.part[(g.tile0 + tm) * g.n + n0 + n] = all;
             }
         } else if constexpr (E == kDiff) {
-            // this wave's part of the tile, [n][m], then [m][n]
+            // this wave's part of the tile, [n][m]
             constexpr int PM = BM / WM, PN = BN / WN;
-            uint16_t *mine = reinterpret_cast<uint16_t *>(stage) + wave * (PM * PN);
+            uint16_t *mine = reinterpret_cast<uint16_t *>(stage) + epi_wave * (PM * PN);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int n = wave_n + j * 16 + lane_n;
@@ -203,13 +356,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             }
             // Chunks of 8 elements are moved within their row by the row's
             // number, so that neither the writes nor the reads meet in a bank.
-            constexpr int CM = PM / 8, CN = PN / 8;
+            constexpr int CM = PM / 8;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
-                    const int n = j * 16 + lane_n, c = i * 2 + (lane >> 5);
-                    *reinterpret_cast<u32x2 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8 + ((lane >> 4) & 1) * 4]) =
+                    const int n = j * 16 + lane_n, c = i * 2 + (epi_lane >> 5);
+                    *reinterpret_cast<u32x2 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8 + ((epi_lane >> 4) & 1) * 4]) =
                         u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
                 }
             __syncthreads();
@@ -217,29 +370,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             const int pad_n = (cols_in + kDepth - 1) / kDepth * kDepth;
 #pragma unroll
             for (int i = 0; i < PN * CM / 64; ++i) {
-                const int n = i * (64 / CM) + lane / CM, c = lane % CM;
-                if (wave_n + n < cols_in && wave_m + c * 8 < pad_m)
+                const int n = i * (64 / CM) + epi_lane / CM, c = epi_lane % CM;
+                if (wave_n + n < pad_n && wave_m + c * 8 < pad_m)
                     *reinterpret_cast<u32x4 *>(&g.d[(n0 + wave_n + n) * g.ldd + m0 + wave_m + c * 8]) =
                         *reinterpret_cast<const u32x4 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8]);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int m = i * 16 + lane_m + r, c = j * 2 + ((lane >> 3) & 1);
-                        mine[m * PN + (c ^ ((m >> 2) & (CN - 1))) * 8 + (lane & 7)] =
-                            uint16_t(__float_as_uint(acc[i][j][r >> 1]) >> (r & 1) * 16);
-                    }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < PM * CN / 64; ++i) {
-                const int m = i * (64 / CN) + lane / CN, c = lane % CN;
-                if (wave_m + m < rows_in && wave_n + c * 8 < pad_n)
-                    *reinterpret_cast<u32x4 *>(&g.dt[(m0 + wave_m + m) * g.lddt + n0 + wave_n + c * 8]) =
-                        *reinterpret_cast<const u32x4 *>(&mine[m * PN + (c ^ ((m >> 2) & (CN - 1))) * 8]);
             }
         } else if constexpr (E == kSum) {
             // rows of the sum are padded to kDepth, so quads never pass their end

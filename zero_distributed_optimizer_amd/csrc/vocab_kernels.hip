@@ -25,8 +25,7 @@ struct Some {
     float v[P];
 };
 
-// kOnce: non-temporally, for what a launch reads once and in no order of
-// addresses (131,072 fp32 rows of 1024 by token: 101 us, 121 without).
+// kOnce: non-temporally, for what a launch reads once.
 template <bool kOnce, typename V>
 __device__ __forceinline__ V load_as(const void *p) {
     if constexpr (kOnce)
@@ -396,7 +395,7 @@ __device__ __forceinline__ void write_row(const RowsArgs &r, uint32_t row, const
     }
 }
 
-template <typename T, int P, bool kAdd>
+template <typename T, int P, bool kAdd, bool kOnce>
 __global__ __launch_bounds__(256) void runs_kernel(SumArgs a) {
     const RowsArgs &r = a.r;
     const int lane = threadIdx.x & 63;
@@ -416,7 +415,7 @@ __global__ __launch_bounds__(256) void runs_kernel(SumArgs a) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int j = j0 + k < named ? j0 + k : named - 1;
-                v[k] = c.any ? load_some<P, true>(x + int64_t(__builtin_amdgcn_readlane(my_pos, j)) * r.stride) : Some<P>{};
+                v[k] = c.any ? load_some<P, kOnce>(x + int64_t(__builtin_amdgcn_readlane(my_pos, j)) * r.stride) : Some<P>{};
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -504,65 +503,28 @@ __global__ __launch_bounds__(256) void join_kernel(SumArgs a) {
 
 // ---- around the cross entropy's products --------------------------------------------------------
 
-// Rows of dim elements, one every `stride`, to rows of kdim, zeros behind.
+// Rows of dim elements, one every `stride`, to `padded` rows of kdim, zeros
+// behind the elements and the rows, and where targets (if given) names no row.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim,
-                                                  int64_t kdim, uint16_t *to) {
+                                                  int64_t kdim, int64_t padded, const int64_t *targets,
+                                                  int64_t vocab, uint16_t *to) {
     const int64_t per = kdim / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < padded * per; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / per, c = i % per * 8;
         const uint16_t *p = from + r * stride + c;
+        bool keep = r < rows;
+        if (keep && targets) {
+            const int64_t target = targets[r];
+            keep = target >= 0 && target < vocab;
+        }
         u32x4 x = {0, 0, 0, 0};
-        if (c + 8 <= dim)
+        if (keep && c + 8 <= dim)
             x = *reinterpret_cast<const loose_u32x4 *>(p);
-        else
+        else if (keep)
             for (int k = 0; k < 7; ++k)
                 if (c + k < dim)
                     x[k >> 1] |= uint32_t(p[k]) << (k & 1) * 16;
         *reinterpret_cast<u32x4 *>(to + r * kdim + c) = x;
-    }
-}
-
-// The transpose: to[c][r] = from[r][c], zero for r in [rows, padded) and where
-// targets (if given) names no row for r. 64 x 64 elements a workgroup.
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t *from, int64_t stride, int64_t rows,
-                                                        int64_t dim, int64_t padded, const int64_t *targets,
-                                                        int64_t vocab, uint16_t *to) {
-    __shared__ uint16_t tile[64][66];
-    const int64_t across = (dim + 63) / 64, tiles = across * (padded / 64);
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t r0 = t / across * 64, c0 = t % across * 64;
-        const int r = threadIdx.x >> 2, part = (threadIdx.x & 3) * 16;
-        bool keep = r0 + r < rows;
-        if (keep && targets) {
-            const int64_t target = targets[r0 + r];
-            keep = target >= 0 && target < vocab;
-        }
-#pragma unroll
-        for (int h = 0; h < 16; h += 8) {
-            const int64_t left = keep ? dim - (c0 + part + h) : 0;
-            u32x4 x = {0, 0, 0, 0};
-            const uint16_t *p = from + (r0 + r) * stride + c0 + part + h;
-            if (left >= 8)
-                x = *reinterpret_cast<const loose_u32x4 *>(p);
-            else
-                for (int i = 0; i < 7; ++i)
-                    if (i < left)
-                        x[i >> 1] |= uint32_t(p[i]) << (i & 1) * 16;
-            for (int i = 0; i < 8; ++i)
-                tile[r][part + h + i] = uint16_t(x[i >> 1] >> (i & 1) * 16);
-        }
-        __syncthreads();
-        const int64_t c = c0 + r;
-        if (c < dim) {
-#pragma unroll
-            for (int h = 0; h < 16; h += 8) {
-                u32x4 x;
-                for (int i = 0; i < 4; ++i)
-                    x[i] = uint32_t(tile[part + h + 2 * i][r]) | uint32_t(tile[part + h + 2 * i + 1][r]) << 16;
-                *reinterpret_cast<u32x4 *>(to + c * padded + r0 + part + h) = x;
-            }
-        }
-        __syncthreads();
     }
 }
 
@@ -618,40 +580,21 @@ unsigned zero_grid(int64_t n) {
     return unsigned(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 8 * kZeroThreads), grid_of(kZeroGroups))));
 }
 
-// W and hidden as the products need them: in place where their rows are 16-byte
-// aligned whole steps, else a copy.
-struct Operands {
-    bool direct;
-    const uint16_t *hidden;
-    int64_t lda, ldb;
-};
-
-Operands operands(const CeArgs &a, const CeLayout &l, hipStream_t stream) {
-    Operands o{};
-    auto aligned = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    o.direct = a.dim % kDepth == 0 && aligned(a.w) && aligned(a.hidden) &&
-               (a.n <= 1 || (a.hidden_stride % 8 == 0 && a.hidden_stride <= int64_t(1) << 21));
-    if (o.direct) {
-        o.hidden = a.hidden;
-        o.ldb = a.n <= 1 ? a.dim : a.hidden_stride;
-    } else {
-        uint16_t *h = reinterpret_cast<uint16_t *>(a.workspace + l.hidden);
-        pack_kernel<<<grid_of(ceil_div(a.n * l.kdim, 2048)), 256, 0, stream>>>(a.hidden, a.hidden_stride, a.n, a.dim,
-                                                                              l.kdim, h);
-        o.hidden = h;
-        o.ldb = l.kdim;
-    }
-    o.lda = l.kdim;   // dim where direct
-    return o;
+void pack(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim, int64_t kdim, int64_t padded,
+          const int64_t *targets, int64_t vocab, uint16_t *to, hipStream_t stream) {
+    pack_kernel<<<grid_of(ceil_div(padded * kdim, 2048)), 256, 0, stream>>>(from, stride, rows, dim, kdim, padded,
+                                                                           targets, vocab, to);
 }
 
-const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, const Operands &o, int64_t row0, int64_t rows,
-                         hipStream_t stream) {
-    if (o.direct)
+// W where it lies serves the products if its rows are whole steps and 16-byte
+// aligned; else they take a copy, piece by piece.
+bool in_place(const CeArgs &a) { return a.dim % kDepth == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0; }
+
+const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64_t rows, hipStream_t stream) {
+    if (in_place(a))
         return a.w + row0 * a.dim;
     uint16_t *w = reinterpret_cast<uint16_t *>(a.workspace + l.w);
-    pack_kernel<<<grid_of(ceil_div(rows * l.kdim, 2048)), 256, 0, stream>>>(a.w + row0 * a.dim, a.dim, rows, a.dim,
-                                                                           l.kdim, w);
+    pack(a.w + row0 * a.dim, a.dim, rows, a.dim, l.kdim, rows, nullptr, 0, w, stream);
     return w;
 }
 
@@ -681,7 +624,14 @@ template <typename T, int P, bool kAdd>
 void launch_sums(const SumArgs &s, hipStream_t stream) {
     const int64_t waves = std::min<int64_t>(4, ceil_div(s.r.dim, 64 * P));
     const unsigned chunks = grid_of(s.chunks);
-    runs_kernel<T, P, kAdd><<<dim3(chunks, unsigned(ceil_div(s.r.dim, 64 * P * waves))), unsigned(64 * waves), 0, stream>>>(s);
+    const dim3 grid(chunks, unsigned(ceil_div(s.r.dim, 64 * P * waves)));
+    // rows that the 256 MB Infinity Cache can hold are mostly still in it
+    // (GPT-2 small's 12 MB: 8.2 us, 10.0 non-temporally); more are not (537 MB:
+    // 121 us, 101 non-temporally)
+    if (P > 1 && s.r.n * s.r.dim * int64_t(sizeof(T)) > int64_t(1) << 28)
+        runs_kernel<T, P, kAdd, (P > 1)><<<grid, unsigned(64 * waves), 0, stream>>>(s);
+    else
+        runs_kernel<T, P, kAdd, false><<<grid, unsigned(64 * waves), 0, stream>>>(s);
     if (s.chunks > 1) {
         constexpr int J = P == 1 ? 1 : 4;   // of fp32
         join_kernel<J, kAdd><<<dim3(chunks, unsigned(ceil_div(s.r.dim, 64 * J))), 256, 0, stream>>>(s);
@@ -746,11 +696,16 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return hipSuccess;
     const CeLayout l = ce_layout(a.n, a.vocab, a.dim);
-    const Operands o = operands(a, l, stream);
     GemmArgs g{};
-    g.b = o.hidden;
-    g.lda = o.lda;
-    g.ldb = o.ldb;
+    g.b = a.hidden;
+    g.ldb = a.n <= 1 ? a.dim : a.hidden_stride;
+    if (a.dim % kDepth || g.ldb % 8 || g.ldb > int64_t(1) << 21 || (reinterpret_cast<uintptr_t>(a.hidden) & 15)) {
+        uint16_t *h = reinterpret_cast<uint16_t *>(a.workspace + l.hidden);
+        pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, a.n, nullptr, 0, h, stream);
+        g.b = h;
+        g.ldb = l.kdim;
+    }
+    g.lda = l.kdim;   // dim where W is used in place
     g.n = a.n;
     g.k = l.kdim;
     g.splits = 1;
@@ -759,10 +714,10 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
     g.part = reinterpret_cast<float2 *>(a.workspace + l.part);
     g.pick = reinterpret_cast<float *>(a.workspace + l.pick);
     // in place, W needs no pieces but for the tiles' numbers
-    const int64_t rows = o.direct ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
+    const int64_t rows = in_place(a) ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
     for (g.row0 = 0; g.row0 < a.vocab; g.row0 += rows) {
         g.m = std::min(rows, a.vocab - g.row0);
-        g.a = piece_of(a, l, o, g.row0, g.m, stream);
+        g.a = piece_of(a, l, g.row0, g.m, stream);
         if (hipError_t e = launch_gemm(kScore, g, stream); e != hipSuccess)
             return e;
         g.tile0 += ceil_div(g.m, tile_rows(g.m, g.n));
@@ -780,21 +735,19 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return hipSuccess;
     const CeLayout l = ce_layout(a.n, a.vocab, a.dim);
-    const Operands o = operands(a, l, stream);
     auto u16 = [&](int64_t at) { return reinterpret_cast<uint16_t *>(a.workspace + at); };
-    uint16_t *hidden_t = u16(l.hidden_t), *w_t = u16(l.w_t), *d = u16(l.d), *dt = u16(l.d_t);
+    uint16_t *hidden = u16(l.hidden), *d = u16(l.d);
     float *sum = reinterpret_cast<float *>(a.workspace + l.sum);
-    const int64_t across = ceil_div(a.dim, 64);
-    if (a.grads)
-        transpose_kernel<<<grid_of(across * (l.npad / 64)), 256, 0, stream>>>(
-            a.hidden, a.hidden_stride, a.n, a.dim, l.npad, a.targets, a.vocab, hidden_t);
+    // hidden with zeros where no target is: whatever those rows hold, nothing of it is left
+    pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, l.npad, a.targets, a.vocab, hidden, stream);
     for (int64_t row0 = 0; row0 < a.vocab; row0 += l.piece) {
-        const int64_t rows = std::min(l.piece, a.vocab - row0), padded = round_up(rows, kDepth);
+        const int64_t rows = std::min(l.piece, a.vocab - row0);
+        const uint16_t *w = piece_of(a, l, row0, rows, stream);
         GemmArgs g{};
-        g.a = piece_of(a, l, o, row0, rows, stream);
-        g.b = o.hidden;
-        g.lda = o.lda;
-        g.ldb = o.ldb;
+        g.a = w;
+        g.b = hidden;
+        g.lda = l.kdim;
+        g.ldb = l.kdim;
         g.m = rows;
         g.n = a.n;
         g.k = l.kdim;
@@ -806,21 +759,17 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
         g.weight = a.grad_loss;
         g.d = d;
         g.ldd = l.vpad;
-        g.dt = dt;
-        g.lddt = l.npad;
         if (hipError_t e = launch_gemm(kDiff, g, stream); e != hipSuccess)
             return e;
         if (a.grad_hidden) {
-            transpose_kernel<<<grid_of(across * (padded / 64)), 256, 0, stream>>>(
-                a.w + row0 * a.dim, a.dim, rows, a.dim, padded, nullptr, 0, w_t);
             GemmArgs h{};
-            h.a = w_t;
+            h.a = w;
             h.b = d;
-            h.lda = padded;
+            h.lda = l.kdim;
             h.ldb = l.vpad;
             h.m = a.dim;
             h.n = a.n;
-            h.k = padded;
+            h.k = rows;
             h.splits = int32_t(l.splits);
             h.sum = sum;
             h.lds = l.kdim;
@@ -830,10 +779,10 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
         }
         if (a.grads) {
             GemmArgs r{};
-            r.a = hidden_t;
-            r.b = dt;
-            r.lda = l.npad;
-            r.ldb = l.npad;
+            r.a = hidden;
+            r.b = d;
+            r.lda = l.kdim;
+            r.ldb = l.vpad;
             r.m = a.dim;
             r.n = rows;
             r.k = l.npad;
