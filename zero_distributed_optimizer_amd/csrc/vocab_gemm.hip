@@ -8,9 +8,9 @@
 // for grad_hidden, hidden and d for W's gradient): gfx950's transposing LDS
 // read gives the instruction its 8 consecutive k of a lane from either, so that
 // no product needs a transposed copy. A workgroup takes a tile of C and steps
-// over k by kStep; a step's part of both operands comes to LDS straight from
-// memory (16 bytes a lane), kSlots steps ahead, and from there to registers one
-// step ahead of the products.
+// over k by kDepth; a step's part of both operands comes to LDS straight from
+// memory (long rows by whole cache lines), one step ahead, and from there to
+// registers half a step ahead of the products.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -50,25 +50,23 @@ __device__ __forceinline__ void copy16_to_lds(const char *base, uint32_t offset,
 // difference would be NaN).
 __device__ __forceinline__ float exp_below(float x, float top) { return x == top ? 1.0f : __expf(x - top); }
 
-constexpr int kStep = 32, kSlots = 4;
-
 // One operand's part of a step in LDS, R rows or columns of C.
 //
-// Long: R rows of kStep elements (64 bytes). The 16-byte chunk c of row r lies at
-// c ^ spread(r), so that the rows that a fragment's read takes at one chunk are
-// in different banks, 8 or 16 of them at a time. The read gives lane l the 8
-// elements of k from (l / 16) * 8 of row l % 16.
+// Long: R rows of kDepth elements (128 bytes). The 16-byte chunk c of row r lies
+// at c ^ spread(r), so that the rows that a fragment's read takes at one chunk
+// are in different banks. The read gives lane l the 8 elements of k from (l / 16)
+// * 8 of row l % 16.
 //
-// Wide: kStep rows of R elements. A transposing read takes, in each 16 lanes, 4
+// Wide: kDepth rows of R elements. A transposing read takes, in each 16 lanes, 4
 // rows of 16 elements, a row's four 8-byte parts from 4 lanes, and gives lane i
 // the 4 rows' element i; two of them are a fragment. The 32-byte unit u of row r
 // lies at u ^ spread(r), so that the 8 rows that 32 lanes read are in different
 // banks.
 template <int R, int kWaves, bool kWide>
 struct Operand {
-    static constexpr int kLoads = R * kStep * 2 / 1024 / kWaves;  // of 1 KB, a wave
-    static constexpr int kRowBytes = kWide ? R * 2 : kStep * 2, kChunks = kRowBytes / 16;
-    const char *base;
+    static constexpr int kLoads = R * kDepth * 2 / 1024 / kWaves;  // of 1 KB, a wave
+    static constexpr int kRowBytes = kWide ? R * 2 : kDepth * 2, kChunks = kRowBytes / 16;
+    const char *base, *from;
     uint32_t off[kLoads];
     int64_t step;   // bytes from one step's part to the next
     uint32_t ld2;   // bytes from row to row
@@ -76,7 +74,7 @@ struct Operand {
     int lane, load0, last_chunk;
 
     static __device__ __forceinline__ int spread(int r) {
-        return kWide ? (r & 3) | ((r >> 3) & 1) << 2 : ((r >> 1) & 3) ^ ((r >> 3) & 1);
+        return kWide ? (r & 3) | ((r >> 3) & 1) << 2 : r & 7;
     }
     __device__ __forceinline__ int row_of(int i) const { return (load0 + i) * (64 / kChunks) + lane / kChunks; }
     // The chunk of its row that lane's 16 bytes of load i come from.
@@ -100,7 +98,7 @@ struct Operand {
         ld2 = uint32_t(ld * 2);
         if constexpr (kWide) {
             base = reinterpret_cast<const char *>(p + k0 * ld + x0);
-            step = ld * 2 * kStep;
+            step = ld * 2 * kDepth;
             left = int(have - k0 < (1 << 30) ? have - k0 : 1 << 30);
             const int64_t chunks = (count - x0 + 7) / 8;   // rows are padded to 8 elements
             last_chunk = chunks < kChunks ? int(chunks) - 1 : kChunks - 1;
@@ -109,7 +107,7 @@ struct Operand {
                 off[i] = uint32_t(row_of(i)) * ld2 + uint32_t(chunk_of(i)) * 16;
         } else {
             base = reinterpret_cast<const char *>(p + x0 * ld + k0);
-            step = kStep * 2;
+            step = kDepth * 2;
             const int last = int(count - x0 < R ? count - x0 : R) - 1;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -118,27 +116,29 @@ struct Operand {
             }
         }
     }
-    __device__ __forceinline__ void load(uint16_t *stage) {
-        if (kWide && left < kStep) {
+    // A step's copies: first next(), then each of them once.
+    __device__ __forceinline__ void next() {
+        if (kWide && left < kDepth) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int r = row_of(i);
                 off[i] = uint32_t(r < left ? r : left - 1) * ld2 + uint32_t(chunk_of(i)) * 16;
             }
         }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            copy16_to_lds(base, off[i], stage + (load0 + i) * 512);
+        from = base;
         base += step;
         if (kWide)
-            left -= kStep;
+            left -= kDepth;
+    }
+    __device__ __forceinline__ void copy(int i, uint16_t *stage) const {
+        copy16_to_lds(from, off[i], stage + (load0 + i) * 512);
     }
 };
 
 // A wave's fragments of an operand: T of 16 rows or columns from x.
 template <int R, int T, bool kWide>
 struct Fragments {
-    int at[kWide ? T : 1];
+    int at[kWide ? T : 2];
 
     __device__ __forceinline__ Fragments(int x, int lane) {
         if constexpr (kWide) {
@@ -147,15 +147,19 @@ struct Fragments {
             for (int i = 0; i < T; ++i)
                 at[i] = r * R + (((x >> 4) + i) ^ spread) * 16 + (lane & 3) * 4;
         } else {
-            at[0] = (x + (lane & 15)) * kStep + ((lane >> 4) ^ Operand<R, 1, false>::spread(lane & 15)) * 8;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                at[half] = (x + (lane & 15)) * kDepth + ((half * 4 + (lane >> 4)) ^ Operand<R, 1, false>::spread(lane & 15)) * 8;
         }
     }
-    __device__ __forceinline__ bf16x8 read(const uint16_t *slot, int i) const {
+    // Of k, the first or the second half.
+    __device__ __forceinline__ bf16x8 read(const uint16_t *stage, int i, int half) const {
         if constexpr (kWide) {
-            const bf16x4 lo = transposed(slot + at[i]), hi = transposed(slot + at[i] + 4 * R);
+            const uint16_t *p = stage + at[i] + half * (kDepth / 2) * R;
+            const bf16x4 lo = transposed(p), hi = transposed(p + 4 * R);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
-            return *reinterpret_cast<const bf16x8 *>(slot + at[0] + i * 16 * kStep);
+            return *reinterpret_cast<const bf16x8 *>(stage + at[half] + i * 16 * kDepth);
         }
     }
     static __device__ __forceinline__ bf16x4 transposed(const uint16_t *p) {
@@ -164,10 +168,10 @@ struct Fragments {
 };
 
 // Waits until at most `kLeft` of this wave's copies to LDS are still on their
-// way, then for the other waves to get here.
+// way and its LDS reads are done, then for the other waves to get here.
 template <int kLeft>
 __device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
 template <int BM, int BN, int WM, int WN, int E>
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WM * WN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles a wave
     constexpr bool kWideA = E == kSum || E == kRows, kWideB = E == kRows;
-    __shared__ __align__(1024) uint16_t stage[kSlots][(BM + BN) * kStep];
+    __shared__ __align__(1024) uint16_t stage[2][(BM + BN) * kDepth];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / WN, wn = wave % WN;
@@ -186,23 +190,23 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
 
     for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
         // The tiles of an XCD (workgroups go to the 8 of them in turn) follow
-        // each other; in that order, 8 tiles along m at each n.
+        // each other; in that order, 4 tiles along m at each n.
         const int each = tiles / 8, more = tiles % 8, x = id % 8;
         int t = x * each + (x < more ? x : more) + id / 8;
         const int split = t / (tiles_m * tiles_n);
         t -= split * tiles_m * tiles_n;
-        const int band = t / (8 * tiles_n), wide = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
-        const int tm = band * 8 + (t - band * 8 * tiles_n) % wide, tn = (t - band * 8 * tiles_n) / wide;
+        const int band = t / (4 * tiles_n), wide = tiles_m - band * 4 < 4 ? tiles_m - band * 4 : 4;
+        const int tm = band * 4 + (t - band * 4 * tiles_n) % wide, tn = (t - band * 4 * tiles_n) / wide;
         const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
 
-        const int steps_all = int((g.k + kStep - 1) / kStep);
+        const int steps_all = int((g.k + kDepth - 1) / kDepth);
         const int first = int(int64_t(steps_all) * split / g.splits);
         const int steps = int(int64_t(steps_all) * (split + 1) / g.splits) - first;
 
         Operand<BM, kWaves, kWideA> a;
         Operand<BN, kWaves, kWideB> b;
-        a.start(g.a, g.lda, m0, g.m, int64_t(first) * kStep, g.k, wave, lane);
-        b.start(g.b, g.ldb, n0, g.n, int64_t(first) * kStep, g.k, wave, lane);
+        a.start(g.a, g.lda, m0, g.m, int64_t(first) * kDepth, g.k, wave, lane);
+        b.start(g.b, g.ldb, n0, g.n, int64_t(first) * kDepth, g.k, wave, lane);
 
         f32x4 acc[TM][TN];
 #pragma unroll
@@ -212,64 +216,74 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                 acc[i][j] = f32x4{0, 0, 0, 0};
 
         constexpr int kCopies = a.kLoads + b.kLoads;   // a wave's, of a step
-        auto copy = [&](int slot) {
-            a.load(stage[slot]);
-            b.load(stage[slot] + BM * kStep);
+        auto next = [&] {
+            a.next();
+            b.next();
+        };
+        auto copy = [&](int i, int s) {
+            if (i < a.kLoads)
+                a.copy(i, stage[s]);
+            else
+                b.copy(i - a.kLoads, stage[s] + BM * kDepth);
         };
         bf16x8 fa[TM], fb[2][TN];
-        // Step k, whose fragments are in registers: its products, and meanwhile
-        // step k + 3's copies and, where an A fragment has been used, step k +
-        // 1's. Step k + 3 goes where step k - 1 was, whose fragments every wave
-        // has had in registers before it got here.
-        auto products = [&](int k, auto set, auto all) {
-            constexpr int kSet = decltype(set)::value;
-            constexpr bool kAll = decltype(all)::value;   // steps k + 1 to k + 3 exist
-            if (kAll || k + 2 < steps)
-                wait_and_meet<kCopies>();
-            else
-                wait_and_meet<0>();
-            if (kAll || k + 3 < steps)
-                copy((k + 3) % kSlots);
-            // (behind the last step: whatever the slot holds, unused)
-            const uint16_t *next = stage[(k + 1) % kSlots];
+        // The products of half a step, whose fragments are in registers (fb[half]),
+        // and meanwhile, where a fragment of A has been used, the next half's
+        // from stage s and, if any, the copies to the other stage.
+        auto products = [&](auto half, int s, auto copies) {
+            constexpr int h = decltype(half)::value;
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
+                if constexpr (decltype(copies)::value)
+#pragma unroll
+                    for (int c = i * kCopies / TM; c < (i + 1) * kCopies / TM; ++c)
+                        copy(c, s ^ 1);
 #pragma unroll
                 for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j)
-                    fb[kSet ^ 1][j] = frag_b.read(next + BM * kStep, j);
+                    fb[h ^ 1][j] = frag_b.read(stage[s] + BM * kDepth, j, h ^ 1);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[kSet][j], acc[i][j], 0, 0, 0);
-                fa[i] = frag_a.read(next, i);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[h][j], acc[i][j], 0, 0, 0);
+                fa[i] = frag_a.read(stage[s], i, h ^ 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
+        constexpr std::integral_constant<int, 0> first_half;
+        constexpr std::integral_constant<int, 1> second_half;
+        constexpr std::true_type copies_yes;
+        constexpr std::false_type copies_no;
         __syncthreads();   // the LDS is free
 #pragma unroll
-        for (int s = 0; s < 3; ++s)
-            if (s < steps)
-                copy(s);
-        if (steps >= 3)
-            wait_and_meet<2 * kCopies>();
+        for (int s = 0; s < 2; ++s)
+            if (s < steps) {
+                next();
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c)
+                    copy(c, s);
+            }
+        if (steps >= 2)
+            wait_and_meet<kCopies>();
         else
             wait_and_meet<0>();
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-            fa[i] = frag_a.read(stage[0], i);
+            fa[i] = frag_a.read(stage[0], i, 0);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            fb[0][j] = frag_b.read(stage[0] + BM * kStep, j);
-        constexpr std::integral_constant<int, 0> even;
-        constexpr std::integral_constant<int, 1> odd;
+            fb[0][j] = frag_b.read(stage[0] + BM * kDepth, j, 0);
         int k = 0;
-        for (; k + 4 < steps; k += 2) {
-            products(k, even, std::true_type());
-            products(k + 1, odd, std::true_type());
+        for (; k + 2 < steps; ++k) {
+            products(first_half, k & 1, copies_no);
+            // step k is in registers in all waves, step k + 1 in LDS
+            wait_and_meet<0>();
+            next();
+            products(second_half, (k + 1) & 1, copies_yes);
         }
-        for (; k < steps; k += 2) {
-            products(k, even, std::false_type());
-            if (k + 1 < steps)
-                products(k + 1, odd, std::false_type());
+        for (; k < steps; ++k) {
+            products(first_half, k & 1, copies_no);
+            wait_and_meet<0>();
+            // (behind the last step the reads get whatever is there: unused)
+            products(second_half, (k + 1) & 1, copies_no);
         }
         __syncthreads();   // LDS serves the epilogue
 
