@@ -26,7 +26,7 @@ GRID_LOOP_LIB = os.path.join(HERE, "libzdo_gridloop.so")
 GRID_LOOP_FLAGS = ["-DZDO_MAX_GRID=64", "-DZDO_MX_WIDE_TILES=1", "-DZDO_MX_LONG_TILES=1"]
 SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "mx_abi.cpp", "mx_kernels.hip", "vocab_abi.cpp", "vocab_kernels.hip",
            "vocab_gemm.hip"]
-HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h", "vocab.h"]
+HEADERS = ["zdo_internal.h", "kernels.h", "device.h", "checks.h", "mx.h", "vocab.h", "vocab_device.h"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

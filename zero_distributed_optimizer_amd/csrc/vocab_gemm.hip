@@ -17,6 +17,7 @@
 
 #include "device.h"
 #include "vocab.h"
+#include "vocab_device.h"
 
 #pragma clang fp contract(off)
 
@@ -46,9 +47,12 @@ __device__ __forceinline__ void copy16_to_lds(const char *base, uint32_t offset,
                  : "memory");
 }
 
-// exp(x - top) that is 1 at the top, whatever the top is (both infinite: the
-// difference would be NaN).
-__device__ __forceinline__ float exp_below(float x, float top) { return x == top ? 1.0f : __expf(x - top); }
+// Where a target's row lies among `count` rows from the piece's row `from` on; -1
+// if it is none of them.
+__device__ __forceinline__ int row_of_target(const GemmArgs &g, int64_t target, int64_t from, int count) {
+    const int64_t r = target - g.row0 - from;
+    return target >= 0 && target < g.vocab && r >= 0 && r < count ? int(r) : -1;
+}
 
 // One operand's part of a step in LDS, R rows or columns of C.
 //
@@ -297,35 +301,44 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
         const int lane_m = (epi_lane >> 4) * 4, lane_n = epi_lane & 15;
         const int rows_in = int(g.m - m0 < BM ? g.m - m0 : BM), cols_in = int(g.n - n0 < BN ? g.n - n0 : BN);
 
+        // all rows of the tile are there: then no element is asked for its row
+        const bool whole = rows_in == BM;
         if constexpr (E == kScore) {
             float2 *red = reinterpret_cast<float2 *>(stage);   // [WM][BN]
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int n = wave_n + j * 16 + lane_n;
-                // the target's row in this tile, if it is in it
-                int64_t target = n < cols_in ? g.targets[n0 + n] : -1;
-                target = target >= 0 && target < g.vocab ? target - g.row0 - m0 : -1;
+                // the target's row, from this wave's first, if it is one of its rows
+                const int target = row_of_target(g, n < cols_in ? g.targets[n0 + n] : -1, m0 + wave_m, BM / WM);
+                if (__any(target >= 0))
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (target == i * 16 + lane_m + r)
+                                g.pick[n0 + n] = acc[i][j][r];
+                if (!whole)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (wave_m + i * 16 + lane_m + r >= rows_in)
+                                acc[i][j][r] = -INFINITY;
                 float top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int m = wave_m + i * 16 + lane_m + r;
-                        if (m < rows_in) {
-                            top = fmaxf(top, acc[i][j][r]);
-                            if (m == target)
-                                g.pick[n0 + n] = acc[i][j][r];
-                        }
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        top = fmaxf(top, acc[i][j][r]);
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
+                const float base = base_of(top);
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (wave_m + i * 16 + lane_m + r < rows_in)
-                            sum += exp_below(acc[i][j][r], top);
+                        sum += __expf(acc[i][j][r] - base);
                 sum += __shfl_xor(sum, 16);
                 sum += __shfl_xor(sum, 32);
                 if (epi_lane < 16)
@@ -336,11 +349,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             if (n < cols_in) {
                 float2 all = red[n];
 #pragma unroll
-                for (int w = 1; w < WM; ++w) {
-                    const float2 one = red[w * BN + n];
-                    const float top = fmaxf(all.x, one.x);
-                    all = {top, all.y * exp_below(all.x, top) + one.y * exp_below(one.x, top)};
-                }
+                for (int w = 1; w < WM; ++w)
+                    all = join_softmax(all, red[w * BN + n]);
                 g.part[(g.tile0 + tm) * g.n + n0 + n] = all;
             }
         } else if constexpr (E == kDiff) {
@@ -350,22 +360,36 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int n = wave_n + j * 16 + lane_n;
-                int64_t target = n < cols_in ? g.targets[n0 + n] : -1;
-                const bool named = target >= 0 && target < g.vocab;
-                target = named ? target - g.row0 - m0 : -1;
+                const int64_t named_row = n < cols_in ? g.targets[n0 + n] : -1;
+                const bool named = named_row >= 0 && named_row < g.vocab;
+                const int target = row_of_target(g, named_row, m0 + wave_m, PM);
                 const float lse = named ? g.lse[n0 + n] : 0.0f, weight = named ? g.weight[n0 + n] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    float v[4];
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int m = wave_m + i * 16 + lane_m + r;
-                        const float p = __expf(acc[i][j][r] - lse);
-                        v[r] = named && m < rows_in ? (m == target ? p - 1.0f : p) * weight : 0.0f;
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][r] = __expf(acc[i][j][r] - lse);
+                if (__any(target >= 0))
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (target == i * 16 + lane_m + r)
+                                acc[i][j][r] -= 1.0f;
+                if (!whole)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (wave_m + i * 16 + lane_m + r >= rows_in)
+                                acc[i][j][r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
                     // four bf16, in the registers of the logits
-                    acc[i][j][0] = __uint_as_float(to_bf16x2(v[0], v[1]));
-                    acc[i][j][1] = __uint_as_float(to_bf16x2(v[2], v[3]));
+                    const uint32_t lo = to_bf16x2(acc[i][j][0] * weight, acc[i][j][1] * weight);
+                    const uint32_t hi = to_bf16x2(acc[i][j][2] * weight, acc[i][j][3] * weight);
+                    acc[i][j][0] = __uint_as_float(named ? lo : 0u);
+                    acc[i][j][1] = __uint_as_float(named ? hi : 0u);
                 }
             }
             // Chunks of 8 elements are moved within their row by the row's

@@ -8,6 +8,7 @@
 
 #include "device.h"
 #include "vocab.h"
+#include "vocab_device.h"
 
 #pragma clang fp contract(off)
 
@@ -533,21 +534,17 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t
 __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *part, int64_t tiles, const float *pick) {
     __shared__ float2 red[16][16];
     const int token = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    auto join = [](float2 x, float2 y) {
-        const float top = fmaxf(x.x, y.x);
-        return float2{top, x.y * (x.x == top ? 1.0f : __expf(x.x - top)) + y.y * (y.x == top ? 1.0f : __expf(y.x - top))};
-    };
     for (int64_t t0 = int64_t(blockIdx.x) * 16; t0 < a.n; t0 += int64_t(gridDim.x) * 16) {
         const int64_t t = t0 + token;
         float2 all = {-INFINITY, 0.0f};
         if (t < a.n)
             for (int64_t k = slice; k < tiles; k += 16)
-                all = join(all, part[k * a.n + t]);
+                all = join_softmax(all, part[k * a.n + t]);
         red[slice][token] = all;
         __syncthreads();
         if (slice == 0 && t < a.n) {
             for (int s = 1; s < 16; ++s)
-                all = join(all, red[s][token]);
+                all = join_softmax(all, red[s][token]);
             const float lse = all.x + logf(all.y);
             const int64_t target = a.targets[t];
             a.lse[t] = lse;
