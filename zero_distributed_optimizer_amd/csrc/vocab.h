@@ -135,18 +135,38 @@ struct GemmArgs {
     int32_t accumulate;
 };
 
-// Tiles are 256 x 256 where those are enough to occupy the chip's 256 compute
-// units, else 128 x 128. The partial results of kScore are laid out for the
-// smaller ones.
+// Tiles are 256 x 256, one workgroup a compute unit, or 128 x 128, two; the partial
+// results of kScore are laid out for the smaller ones. Which of them, how many
+// splits and pieces: by the time that rounds of tiles over the chip's 256 compute
+// units take, kRoundK for each k of a round of large tiles (1.3 PFLOP/s) and
+// kRoundOwn of its own for each round, in us. A round of 512 small tiles has half
+// the work and takes 0.62 of a large one's time, of 256 and fewer 0.4 (loss of
+// 128 tokens of Llama-3-8B by small tiles 195 us, by large ones 238; 8,192 tokens
+// of GPT-2 small 778 and 646; the gradients of 16,384 tokens with this choice
+// 4.49 ms, at 0.5 and 0.3 4.61, at 1.1 and 0.9 5.00).
 constexpr int kTileRowsMin = 128;
+constexpr double kRoundK = 0.026, kRoundOwn = 5.0;
+inline double wide_rounds(int64_t m, int64_t n, int64_t splits) {
+    return double(ceil_div(ceil_div(m, 256) * ceil_div(n, 256) * splits, 256));
+}
+inline double small_rounds(int64_t m, int64_t n, int64_t splits) {
+    const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128) * splits;
+    return 0.62 * double(tiles / 512) + (tiles % 512 > 256 ? 0.62 : tiles % 512 ? 0.4 : 0.0);
+}
 inline bool wide_tiles(int64_t m, int64_t n, int64_t splits) {
-    return ceil_div(m, 256) * ceil_div(n, 256) * splits >= 192;
+    return wide_rounds(m, n, splits) <= small_rounds(m, n, splits);
 }
 inline int64_t tile_rows(int64_t m, int64_t n) { return wide_tiles(m, n, 1) ? 256 : kTileRowsMin; }
+inline double product_us(int64_t m, int64_t n, int64_t k, int64_t splits) {
+    return std::min(wide_rounds(m, n, splits), small_rounds(m, n, splits)) *
+           (kRoundOwn + kRoundK * double(ceil_div(k, splits)));
+}
 
-#ifndef ZP
-#define ZP 27
-#endif
+// The loss of up to kThinTokens tokens may go by thin_score_kernel, kThinRows rows
+// of W a tile.
+constexpr int64_t kThinTokens = 32;
+constexpr int kThinRows = 64;
+
 // A call's workspace. The vocabulary is taken in pieces of `piece` rows: at most
 // 2^27 elements of d (256 MB, the size of the Infinity Cache that they go
 // through to the two products that read them), but at least 256 rows, and at
@@ -157,24 +177,31 @@ struct CeLayout {
     int64_t hidden, w, d, sum, part, pick, bytes;
 };
 
-// Splits of the sum over the vocabulary that grad_hidden is: as many as give
-// the chip's 256 compute units a tile each, but steps of at least 16 * kDepth
-// rows.
-inline int64_t hidden_splits(int64_t n, int64_t dim, int64_t piece) {
-    const int64_t tiles = ceil_div(n, 256) * ceil_div(dim, 256);
-    return std::max<int64_t>(1, std::min(256 / tiles, piece / (16 * kDepth)));
-}
-
 inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     CeLayout l{};
+    const int64_t some = std::max<int64_t>(n, 1);
     l.kdim = round_up(dim, kDepth);
-    l.npad = round_up(std::max<int64_t>(n, 1), kDepth);
-    int64_t most = std::min((int64_t(1) << ZP) / l.npad, (int64_t(1) << 27) / l.kdim);
+    l.npad = round_up(some, kDepth);
+    int64_t most = std::min((int64_t(1) << 27) / l.npad, (int64_t(1) << 27) / l.kdim);
     most = std::max<int64_t>(256, most / 256 * 256);
-    const int64_t pieces = ceil_div(vocab, most);
-    l.piece = std::min(vocab, round_up(ceil_div(vocab, pieces), 256));
+    // the number of pieces, at least this many, and of splits of grad_hidden's sum
+    // over the vocabulary (each adds to an fp32 sum of its own at 5 TB/s)
+    const int64_t least = ceil_div(vocab, most);
+    double best = 0.0;
+    for (int64_t p = least; p < least + 4 && p <= vocab; ++p) {
+        const int64_t piece = std::min(vocab, round_up(ceil_div(vocab, p), 256));
+        const double rest = product_us(piece, some, dim, 1) + product_us(dim, piece, some, 1);
+        for (int64_t s = 1; s == 1 || (s <= piece / 256 && s * some * l.kdim <= int64_t(1) << 25); s += s < 4 ? 1 : s / 2) {
+            const double us = double(ceil_div(vocab, piece)) *
+                              (rest + product_us(dim, some, piece, s) + double(s * some * dim) * 8 / 5e6);
+            if (best == 0.0 || us < best) {
+                best = us;
+                l.piece = piece;
+                l.splits = s;
+            }
+        }
+    }
     l.vpad = round_up(l.piece, kDepth);
-    l.splits = hidden_splits(std::max<int64_t>(n, 1), dim, l.piece);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -185,7 +212,8 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     l.w = take(2 * l.piece * l.kdim);
     const int64_t both = at;
     // the loss
-    l.part = take(8 * n * (ceil_div(vocab, l.piece) * ceil_div(l.piece, kTileRowsMin)));
+    const int64_t tiles = ceil_div(vocab, l.piece) * ceil_div(l.piece, kTileRowsMin);
+    l.part = take(8 * n * (n <= kThinTokens ? std::max(tiles, ceil_div(vocab, kThinRows)) : tiles));
     l.pick = take(4 * n);
     const int64_t loss = at;
     // its gradient
@@ -220,6 +248,7 @@ hipError_t launch_lookup(const LookupArgs &a, hipStream_t stream);
 hipError_t launch_rows(const RowsArgs &a, hipStream_t stream);
 hipError_t launch_ce(const CeArgs &a, hipStream_t stream);
 hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream);
+hipError_t launch_thin_score(const GemmArgs &a, hipStream_t stream);
 hipError_t launch_gemm(Epilogue e, const GemmArgs &a, hipStream_t stream);
 
 // Elements [0, n) to zero.

@@ -1,4 +1,5 @@
-// What the vocabulary matrix's device files share: the softmax's statistics.
+// What the vocabulary matrix's device files share: accesses of rows that start at
+// any element, and the softmax's statistics.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +10,12 @@
 
 namespace zdo {
 namespace {
+
+// 16 and 8 bytes at any address that is aligned to an element; gfx950 takes them in
+// one instruction.
+typedef u32x4 loose_u32x4 __attribute__((aligned(2)));
+typedef u32x2 loose_u32x2 __attribute__((aligned(2)));
+typedef f32x4 loose_f32x4 __attribute__((aligned(4)));
 
 // What the exponentials of values up to `top` are taken relative to: `top`, or 0
 // where that is infinite (the difference would be NaN: the sum is then 0 or

@@ -27,12 +27,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-// 8 or 16 bytes at any address that is aligned to an element.
-template <typename V>
-struct __attribute__((packed, aligned(2))) Loose {
-    V v;
-};
-
 // 16 bytes a lane from base + its offset to LDS, lane after lane from `to` (the
 // same for the whole wave) on. Written as an instruction, because the compiler
 // would wait for all such copies before every LDS read (it cannot tell the slots
@@ -442,12 +436,12 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                         continue;
                     f32x4 v = acc[i][j];
                     if (m + 4 <= rows_in) {
-                        Loose<u32x2> *at = reinterpret_cast<Loose<u32x2> *>(row + m);
+                        loose_u32x2 *at = reinterpret_cast<loose_u32x2 *>(row + m);
                         if (g.accumulate) {
-                            const u32x2 old = at->v;
+                            const u32x2 old = *at;
                             v += f32x4{lo_f32(old.x), hi_f32(old.x), lo_f32(old.y), hi_f32(old.y)};
                         }
-                        at->v = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
+                        *at = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
                     } else {
                         for (int r = 0; r < rows_in - m; ++r) {
                             const float x = r == 0 ? v[0] : r == 1 ? v[1] : v[2];
@@ -457,6 +451,161 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                 }
             }
         }
+    }
+}
+
+// The logits' statistics for few tokens, where reading W is all there is to do: a
+// workgroup takes kThinRows rows of W, each of its 4 waves a quarter of k, and
+// reads W from memory to registers as the instruction takes it (lane l: 16 bytes
+// of row l % 16), the next 64 k while it multiplies these. Rows start anywhere
+// and have any length; hidden comes out of the caches. The quarters are added
+// through LDS.
+template <int TN>
+__global__ __launch_bounds__(256, 2) void thin_score_kernel(GemmArgs g) {
+    constexpr int TM = kThinRows / 16;
+    __shared__ f32x4 quarter[4][TM * TN][64];
+    __shared__ float2 red[TM][TN * 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = int((g.m + kThinRows - 1) / kThinRows);
+    const int64_t steps = g.k / 64, first = steps * wave / 4, last = steps * (wave + 1) / 4;   // and the rest of k
+
+    // 8 elements from c on of a row of g.k, zeros behind its end: the row's last 8,
+    // moved down
+    auto load8 = [&](const uint16_t *row, int64_t c) {
+        const int64_t past = c + 8 - g.k;   // of the 8
+        u32x4 x = {0, 0, 0, 0};
+        if (past >= 8)
+            return x;
+        if (g.k < 8) {
+            for (int i = 0; i < 7; ++i)
+                if (c + i < g.k)
+                    x[i >> 1] |= uint32_t(row[c + i]) << (i & 1) * 16;
+            return x;
+        }
+        x = *reinterpret_cast<const loose_u32x4 *>(row + (past > 0 ? g.k - 8 : c));
+        if (past > 0) {
+            uint64_t lo = uint64_t(x.y) << 32 | x.x, hi = uint64_t(x.w) << 32 | x.z;
+            const int s = int(past) * 16;
+            lo = s >= 64 ? hi >> (s - 64) : lo >> s | hi << (64 - s);
+            hi = s >= 64 ? 0 : hi >> s;
+            x = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+        }
+        return x;
+    };
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t m0 = int64_t(tile) * kThinRows;
+        const int rows_in = int(g.m - m0 < kThinRows ? g.m - m0 : kThinRows);
+        // what lies behind the last row or token is read as the last, and not kept
+        const uint16_t *a[TM], *b[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = i * 16 + (lane & 15);
+            a[i] = g.a + (m0 + (r < rows_in ? r : rows_in - 1)) * g.lda;
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t n = j * 16 + (lane & 15);
+            b[j] = g.b + (n < g.n ? n : g.n - 1) * g.ldb;
+        }
+        f32x4 acc[TM][TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = f32x4{0, 0, 0, 0};
+        u32x4 fa[2][2][TM], fb[2][2][TN];
+        auto load = [&](int set, int64_t step) {
+            const int64_t c = step * 64 + (lane >> 4) * 16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    fa[set][h][i] = *reinterpret_cast<const loose_u32x4 *>(a[i] + c + h * 8);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    fb[set][h][j] = *reinterpret_cast<const loose_u32x4 *>(b[j] + c + h * 8);
+            }
+        };
+        auto products = [&](int set) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, fa[set][h][i]), __builtin_bit_cast(bf16x8, fb[set][h][j]),
+                            acc[i][j], 0, 0, 0);
+        };
+        if (first < last)
+            load(0, first);
+        for (int64_t k = first; k < last; k += 2) {
+            if (k + 1 < last)
+                load(1, k + 1);
+            products(0);
+            if (k + 1 >= last)
+                break;
+            if (k + 2 < last)
+                load(0, k + 2);
+            products(1);
+        }
+        if (wave == 3 && g.k % 64) {
+            const int64_t c = g.k / 64 * 64 + (lane >> 4) * 16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    fa[0][h][i] = load8(a[i], c + h * 8);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    fb[0][h][j] = load8(b[j], c + h * 8);
+            }
+            products(0);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                quarter[wave][i * TN + j][lane] = acc[i][j];
+        __syncthreads();
+        // wave i: rows i * 16 + lane / 16 * 4 + r
+        static_assert(TM == 4, "a wave for each 16 rows");
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            f32x4 z = quarter[0][wave * TN + j][lane];
+            for (int w = 1; w < 4; ++w)
+                z += quarter[w][wave * TN + j][lane];
+            const int n = j * 16 + (lane & 15), m = wave * 16 + (lane >> 4) * 4;
+            const int target = row_of_target(g, n < g.n ? g.targets[n] : -1, m0, kThinRows);
+            float top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (m + r >= rows_in)
+                    z[r] = -INFINITY;
+                else if (m + r == target)
+                    g.pick[n] = z[r];
+                top = fmaxf(top, z[r]);
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                sum += __expf(z[r] - base_of(top));
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lane < 16)
+                red[wave][n] = {top, sum};
+        }
+        __syncthreads();
+        const int n = threadIdx.x;
+        if (n < g.n) {
+            float2 all = red[0][n];
+            for (int w = 1; w < TM; ++w)
+                all = join_softmax(all, red[w][n]);
+            g.part[(g.tile0 + tile) * g.n + n] = all;
+        }
+        __syncthreads();
     }
 }
 
@@ -478,6 +627,15 @@ hipError_t launch_sized(const GemmArgs &g, hipStream_t stream) {
 }
 
 }  // namespace
+
+hipError_t launch_thin_score(const GemmArgs &g, hipStream_t stream) {
+    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(g.m, kThinRows), std::min<int64_t>(kMaxGrid, 1 << 21)));
+    if (g.n <= 16)
+        thin_score_kernel<1><<<grid, 256, 0, stream>>>(g);
+    else
+        thin_score_kernel<2><<<grid, 256, 0, stream>>>(g);
+    return hipGetLastError();
+}
 
 hipError_t launch_gemm(Epilogue e, const GemmArgs &g, hipStream_t stream) {
     if (g.m <= 0 || g.n <= 0)

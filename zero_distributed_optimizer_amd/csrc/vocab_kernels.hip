@@ -1,9 +1,6 @@
 // Device kernels at the vocabulary matrix (zdo_vocab.h) for gfx950: the
 // embedding lookup, its gradient over sorted tokens, and what surrounds the
 // cross entropy's products (vocab_gemm.hip).
-//
-// Rows of the matrix start at any element, so 16-byte accesses are written
-// for 2-byte alignment; gfx950 takes them in one instruction.
 #include <hip/hip_runtime.h>
 
 #include "device.h"
@@ -14,10 +11,6 @@
 
 namespace zdo {
 namespace {
-
-typedef u32x4 loose_u32x4 __attribute__((aligned(2)));
-typedef u32x2 loose_u32x2 __attribute__((aligned(2)));
-typedef f32x4 loose_f32x4 __attribute__((aligned(4)));
 
 // P consecutive elements of a row, widened: those of a 16-byte access, or 1
 // where a row has fewer.
@@ -529,22 +522,35 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t
     }
 }
 
-// The softmax's statistics of all tiles to each token's loss and lse: 16
-// tokens a workgroup, 16 threads each over every 16th tile.
+// The softmax's statistics of all tiles to each token's loss and lse: kTokens of
+// them a workgroup, 256 / kTokens threads each over the tiles in turn.
+template <int kTokens>
 __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *part, int64_t tiles, const float *pick) {
-    __shared__ float2 red[16][16];
-    const int token = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    for (int64_t t0 = int64_t(blockIdx.x) * 16; t0 < a.n; t0 += int64_t(gridDim.x) * 16) {
+    constexpr int kEach = 256 / kTokens;
+    __shared__ float2 red[kEach][kTokens];
+    const int token = threadIdx.x % kTokens, slice = threadIdx.x / kTokens;
+    for (int64_t t0 = int64_t(blockIdx.x) * kTokens; t0 < a.n; t0 += int64_t(gridDim.x) * kTokens) {
         const int64_t t = t0 + token;
         float2 all = {-INFINITY, 0.0f};
         if (t < a.n)
-            for (int64_t k = slice; k < tiles; k += 16)
-                all = join_softmax(all, part[k * a.n + t]);
+            for (int64_t k = slice; k < tiles; k += 8 * kEach) {
+                float2 x[8];   // loads first
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    x[u] = k + u * kEach < tiles ? part[(k + u * kEach) * a.n + t] : float2{-INFINITY, 0.0f};
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    all = join_softmax(all, x[u]);
+            }
         red[slice][token] = all;
         __syncthreads();
+        for (int half = kEach / 2; half > 0; half /= 2) {
+            if (slice < half)
+                red[slice][token] = join_softmax(red[slice][token], red[slice + half][token]);
+            __syncthreads();
+        }
         if (slice == 0 && t < a.n) {
-            for (int s = 1; s < 16; ++s)
-                all = join_softmax(all, red[s][token]);
+            all = red[0][token];
             const float lse = all.x + logf(all.y);
             const int64_t target = a.targets[t];
             a.lse[t] = lse;
@@ -586,6 +592,12 @@ void pack(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim, int64
 // W where it lies serves the products if its rows are whole steps and 16-byte
 // aligned; else they take a copy, piece by piece.
 bool in_place(const CeArgs &a) { return a.dim % kDepth == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0; }
+
+// Few tokens and W not in place: its rows are read as they lie by
+// thin_score_kernel rather than copied (16 tokens of Llama-3-8B, W off by an
+// element: 482 us, 660 with the copy; 10,007 rows of 1,537: 31 and 40. In place
+// the products are as fast: 184 and 182, GPT-2 small 23.5 and 21.8).
+bool by_rows(const CeArgs &a) { return a.n <= kThinTokens && !in_place(a); }
 
 const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64_t rows, hipStream_t stream) {
     if (in_place(a))
@@ -696,30 +708,46 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
     GemmArgs g{};
     g.b = a.hidden;
     g.ldb = a.n <= 1 ? a.dim : a.hidden_stride;
-    if (a.dim % kDepth || g.ldb % 8 || g.ldb > int64_t(1) << 21 || (reinterpret_cast<uintptr_t>(a.hidden) & 15)) {
-        uint16_t *h = reinterpret_cast<uint16_t *>(a.workspace + l.hidden);
-        pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, a.n, nullptr, 0, h, stream);
-        g.b = h;
-        g.ldb = l.kdim;
-    }
-    g.lda = l.kdim;   // dim where W is used in place
     g.n = a.n;
-    g.k = l.kdim;
     g.splits = 1;
     g.targets = a.targets;
     g.vocab = a.vocab;
     g.part = reinterpret_cast<float2 *>(a.workspace + l.part);
     g.pick = reinterpret_cast<float *>(a.workspace + l.pick);
-    // in place, W needs no pieces but for the tiles' numbers
-    const int64_t rows = in_place(a) ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
-    for (g.row0 = 0; g.row0 < a.vocab; g.row0 += rows) {
-        g.m = std::min(rows, a.vocab - g.row0);
-        g.a = piece_of(a, l, g.row0, g.m, stream);
-        if (hipError_t e = launch_gemm(kScore, g, stream); e != hipSuccess)
+    int64_t tiles = 0;
+    if (by_rows(a)) {
+        g.a = a.w;
+        g.lda = a.dim;
+        g.m = a.vocab;
+        g.k = a.dim;
+        if (hipError_t e = launch_thin_score(g, stream); e != hipSuccess)
             return e;
-        g.tile0 += ceil_div(g.m, tile_rows(g.m, g.n));
+        tiles = ceil_div(g.m, kThinRows);
+    } else {
+        if (a.dim % kDepth || g.ldb % 8 || g.ldb > int64_t(1) << 21 || (reinterpret_cast<uintptr_t>(a.hidden) & 15)) {
+            uint16_t *h = reinterpret_cast<uint16_t *>(a.workspace + l.hidden);
+            pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, a.n, nullptr, 0, h, stream);
+            g.b = h;
+            g.ldb = l.kdim;
+        }
+        g.lda = l.kdim;   // dim where W is used in place
+        g.k = l.kdim;
+        // in place, W needs no pieces but for the tiles' numbers
+        const int64_t rows = in_place(a) ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
+        for (g.row0 = 0; g.row0 < a.vocab; g.row0 += rows) {
+            g.m = std::min(rows, a.vocab - g.row0);
+            g.a = piece_of(a, l, g.row0, g.m, stream);
+            g.tile0 = tiles;
+            if (hipError_t e = launch_gemm(kScore, g, stream); e != hipSuccess)
+                return e;
+            tiles += ceil_div(g.m, tile_rows(g.m, g.n));
+        }
     }
-    combine_kernel<<<grid_of(ceil_div(a.n, 16)), 256, 0, stream>>>(a, g.part, g.tile0, g.pick);
+    // few tokens: a workgroup each
+    if (a.n <= 512)
+        combine_kernel<1><<<grid_of(a.n), 256, 0, stream>>>(a, g.part, tiles, g.pick);
+    else
+        combine_kernel<16><<<grid_of(ceil_div(a.n, 16)), 256, 0, stream>>>(a, g.part, tiles, g.pick);
     return hipGetLastError();
 }
 
