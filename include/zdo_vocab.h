@@ -94,10 +94,11 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
  *   d_i[v]      = (exp(z_i[v] - lse_i) - [v == targets_i]) * grad_loss_i
  *   grad_hidden_i = sum over v of d_i[v] * W[v]   (rounded to grad_hidden_type)
  *   W's gradient: row v = sum over i of d_i[v] * hidden_i   (into grads)
- * z is formed again, in pieces of the vocabulary. d is rounded to bf16 before
- * the two products (relative 2^-9 a term, as the results are rounded), whose
- * sums are in fp32. A token whose target names no row has a grad_hidden of
- * zero. grad_hidden or grads may be NULL (not both): that gradient is not
+ * z is formed again, in pieces of the vocabulary. d is rounded to bf16 for the
+ * two products, as their results are, and the products' sums are in fp32; what
+ * the rounding leaves of d_i[targets_i], the largest term of most sums, is added
+ * to grad_hidden in fp32, and for up to 128 tokens W's gradient takes d in two
+ * bf16 parts. A token whose target names no row has a grad_hidden of zero. grad_hidden or grads may be NULL (not both): that gradient is not
  * computed. hidden's rows of tokens whose target names no row are not used.
  * Outputs and workspace must not overlap the inputs or each other. */
 int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,

@@ -120,10 +120,13 @@ struct GemmArgs {
     float2 *part;
     int64_t tile0;  // the piece's first tile
     float *pick;
-    // kDiff: d, [n][m], zero up to the next multiple of kDepth of both
+    // kDiff: d in bf16, [n][m], zero up to the next multiple of kDepth of both; if
+    // not NULL, low: what that rounding left, in bf16; rest: of the target's d, what
+    // the rounding left
     const float *lse, *weight;
-    uint16_t *d;
+    uint16_t *d, *low;
     int64_t ldd;
+    float *rest;
 
     // kSum: fp32 [split][n][lds], added to what is there unless `first`
     float *sum;
@@ -167,6 +170,11 @@ inline double product_us(int64_t m, int64_t n, int64_t k, int64_t splits) {
 constexpr int64_t kThinTokens = 32;
 constexpr int kThinRows = 64;
 
+// W's gradient of up to this many tokens takes d in two parts, the bf16 number
+// nearest to it and what is left: its sums are then too short for the roundings to
+// cancel, and its time is that of writing the gradient.
+constexpr int64_t kTwoPartTokens = 128;
+
 // A call's workspace. The vocabulary is taken in pieces of `piece` rows: at most
 // 2^27 elements of d (256 MB, the size of the Infinity Cache that they go
 // through to the two products that read them), but at least 256 rows, and at
@@ -174,7 +182,8 @@ constexpr int kThinRows = 64;
 struct CeLayout {
     int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
     int64_t splits;                   // of grad_hidden's sum
-    int64_t hidden, w, d, sum, part, pick, bytes;
+    int64_t parts;                    // of d: 2 for few tokens
+    int64_t hidden, w, d, rest, sum, part, pick, bytes;
 };
 
 inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
@@ -208,7 +217,8 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
         at += round_up(bytes, 256);
         return here;
     };
-    l.hidden = take(2 * l.npad * l.kdim);
+    l.parts = n <= kTwoPartTokens ? 2 : 1;
+    l.hidden = take(2 * l.parts * l.npad * l.kdim);
     l.w = take(2 * l.piece * l.kdim);
     const int64_t both = at;
     // the loss
@@ -218,7 +228,8 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     const int64_t loss = at;
     // its gradient
     at = both;
-    l.d = take(2 * l.npad * l.vpad);
+    l.d = take(2 * l.parts * l.npad * l.vpad);
+    l.rest = take(4 * n);
     l.sum = take(4 * l.splits * n * l.kdim);
     l.bytes = std::max<int64_t>(std::max(at, loss), 256);
     return l;

@@ -351,6 +351,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             // this wave's part of the tile, [n][m]
             constexpr int PM = BM / WM, PN = BN / WN;
             uint16_t *mine = reinterpret_cast<uint16_t *>(stage) + epi_wave * (PM * PN);
+            uint32_t packed[4];
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int n = wave_n + j * 16 + lane_n;
@@ -368,8 +369,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (target == i * 16 + lane_m + r)
+                            if (target == i * 16 + lane_m + r) {
                                 acc[i][j][r] -= 1.0f;
+                                const float d = acc[i][j][r] * weight;
+                                g.rest[n0 + n] = d - lo_f32(to_bf16x2(d, 0.0f));
+                            }
                 if (!whole)
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
@@ -379,33 +383,47 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                                 acc[i][j][r] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
-                    // four bf16, in the registers of the logits
-                    const uint32_t lo = to_bf16x2(acc[i][j][0] * weight, acc[i][j][1] * weight);
-                    const uint32_t hi = to_bf16x2(acc[i][j][2] * weight, acc[i][j][3] * weight);
-                    acc[i][j][0] = __uint_as_float(named ? lo : 0u);
-                    acc[i][j][1] = __uint_as_float(named ? hi : 0u);
+                    // four bf16, and what their rounding left as four more, in the
+                    // registers of the logits
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = acc[i][j][2 * h] * weight, y = acc[i][j][2 * h + 1] * weight;
+                        const uint32_t high = to_bf16x2(x, y), low = to_bf16x2(x - lo_f32(high), y - hi_f32(high));
+                        packed[h] = named ? high : 0u;
+                        packed[2 + h] = named ? low : 0u;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][r] = __uint_as_float(packed[r]);
                 }
             }
             // Chunks of 8 elements are moved within their row by the row's
             // number, so that neither the writes nor the reads meet in a bank.
             constexpr int CM = PM / 8;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int n = j * 16 + lane_n, c = i * 2 + (epi_lane >> 5);
-                    *reinterpret_cast<u32x2 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8 + ((epi_lane >> 4) & 1) * 4]) =
-                        u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
-                }
-            __syncthreads();
             const int pad_m = (rows_in + kDepth - 1) / kDepth * kDepth;
             const int pad_n = (cols_in + kDepth - 1) / kDepth * kDepth;
+            for (int part = 0; part < (g.low ? 2 : 1); ++part) {
+                uint16_t *out = part ? g.low : g.d;
+                if (part)
+                    __syncthreads();
 #pragma unroll
-            for (int i = 0; i < PN * CM / 64; ++i) {
-                const int n = i * (64 / CM) + epi_lane / CM, c = epi_lane % CM;
-                if (wave_n + n < pad_n && wave_m + c * 8 < pad_m)
-                    *reinterpret_cast<u32x4 *>(&g.d[(n0 + wave_n + n) * g.ldd + m0 + wave_m + c * 8]) =
-                        *reinterpret_cast<const u32x4 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8]);
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {
+                        const int n = j * 16 + lane_n, c = i * 2 + (epi_lane >> 5);
+                        *reinterpret_cast<u32x2 *>(
+                            &mine[n * PM + (c ^ (n & (CM - 1))) * 8 + ((epi_lane >> 4) & 1) * 4]) =
+                            part ? u32x2{__float_as_uint(acc[i][j][2]), __float_as_uint(acc[i][j][3])}
+                                 : u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < PN * CM / 64; ++i) {
+                    const int n = i * (64 / CM) + epi_lane / CM, c = epi_lane % CM;
+                    if (wave_n + n < pad_n && wave_m + c * 8 < pad_m)
+                        *reinterpret_cast<u32x4 *>(&out[(n0 + wave_n + n) * g.ldd + m0 + wave_m + c * 8]) =
+                            *reinterpret_cast<const u32x4 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8]);
+                }
             }
         } else if constexpr (E == kSum) {
             // rows of the sum are padded to kDepth, so quads never pass their end

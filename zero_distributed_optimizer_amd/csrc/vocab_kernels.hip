@@ -560,18 +560,25 @@ __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *pa
     }
 }
 
-// The splits' sums of grad_hidden, added in their order and rounded.
+// The splits' sums of grad_hidden, added in their order, and the rest of the
+// target's d times its row; rounded. So the largest term of most sums is exact.
 template <typename T, int P>
-__global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum, int64_t splits, int64_t kdim) {
+__global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum, int64_t splits, int64_t kdim,
+                                                    const float *rest) {
     const int64_t per = (a.dim + P - 1) / P;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.n * per; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / per;
         const Columns<P> c(i % per * P, a.dim);
         const int64_t target = a.targets[r];
         Some<P> e{};
-        if (target >= 0 && target < a.vocab)
+        if (target >= 0 && target < a.vocab) {
+            const Some<P> w = load_some<P>(a.w + target * a.dim + c.at);
             for (int64_t s = 0; s < splits; ++s)
                 add(e, load_some<P, true>(sum + (s * a.n + r) * kdim + c.at));
+            const float x = rest[r];
+            for (int k = 0; k < P; ++k)
+                e.v[k] += x * w.v[k];
+        }
         store_some(static_cast<T *>(a.grad_hidden) + r * a.grad_hidden_stride + c.at, e);
     }
 }
@@ -764,7 +771,10 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     uint16_t *hidden = u16(l.hidden), *d = u16(l.d);
     float *sum = reinterpret_cast<float *>(a.workspace + l.sum);
     // hidden with zeros where no target is: whatever those rows hold, nothing of it is left
-    pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, l.npad, a.targets, a.vocab, hidden, stream);
+    for (int64_t part = 0; part < (a.grads ? l.parts : 1); ++part)
+        pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, l.npad, a.targets, a.vocab,
+             hidden + part * l.npad * l.kdim, stream);
+    float *rest = reinterpret_cast<float *>(a.workspace + l.rest);
     for (int64_t row0 = 0; row0 < a.vocab; row0 += l.piece) {
         const int64_t rows = std::min(l.piece, a.vocab - row0);
         const uint16_t *w = piece_of(a, l, row0, rows, stream);
@@ -783,7 +793,9 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
         g.lse = a.lse;
         g.weight = a.grad_loss;
         g.d = d;
+        g.low = a.grads && l.parts == 2 ? d + l.npad * l.vpad : nullptr;
         g.ldd = l.vpad;
+        g.rest = rest;
         if (hipError_t e = launch_gemm(kDiff, g, stream); e != hipSuccess)
             return e;
         if (a.grad_hidden) {
@@ -810,7 +822,7 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
             r.ldb = l.vpad;
             r.m = a.dim;
             r.n = rows;
-            r.k = l.npad;
+            r.k = l.parts * l.npad;
             r.splits = 1;
             r.rows = a.grads + row0 * a.dim;
             r.accumulate = a.accumulate;
@@ -820,7 +832,7 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     }
     if (a.grad_hidden) {
         const unsigned grid = grid_of(ceil_div(a.n * l.kdim, 2048));
-        auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a, sum, l.splits, l.kdim); };
+        auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a, sum, l.splits, l.kdim, rest); };
         if (a.f32)
             a.dim >= 8 ? go(hidden_kernel<float, 8>) : go(hidden_kernel<float, 1>);
         else
