@@ -131,48 +131,13 @@ __device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
     return token >= 0 && token < vocab ? uint32_t(token) : uint32_t(vocab);
 }
 
-// Zeros to [0, n) by 256 threads of each of the launch's workgroups from
-// `first` on; the first of those also writes the few elements before and behind
-// 16-byte alignment. Few writers are faster than many: 1 GB by 256 workgroups
-// in 160 us, by 512 in 195, by 4096 in 232, non-temporally in 166 to 264.
-struct ZeroArgs {
-    uint16_t *p;
-    int64_t n;
-    int32_t first;  // workgroups before it do something else
-};
-constexpr int kZeroThreads = 256, kZeroGroups = 256;
-
-__device__ __forceinline__ void fill_zero(const ZeroArgs &z) {
-    if (threadIdx.x >= kZeroThreads)
-        return;
-    const int64_t head = (16 - (reinterpret_cast<uintptr_t>(z.p) & 15)) % 16 / 2, from = head < z.n ? head : z.n;
-    const int64_t chunks = (z.n - from) / 8, upto = from + chunks * 8;
-    if (int(blockIdx.x) == z.first) {
-        if (int64_t(threadIdx.x) < from)
-            z.p[threadIdx.x] = 0;
-        if (upto + threadIdx.x < z.n)
-            z.p[upto + threadIdx.x] = 0;
-    }
-    u32x4 *q = reinterpret_cast<u32x4 *>(z.p + from);
-    const int64_t step = int64_t(gridDim.x - z.first) * kZeroThreads;
-    for (int64_t i = int64_t(blockIdx.x - z.first) * kZeroThreads + threadIdx.x; i < chunks; i += step)
-        q[i] = u32x4{0, 0, 0, 0};
-}
-
-__global__ __launch_bounds__(kZeroThreads) void zero_kernel(ZeroArgs z) { fill_zero(z); }
-
 // Few positions: a position's place is the number of keys below its own, or
 // equal and before it. A workgroup counts for 32 positions, a lane each, each
 // half of its 16 waves over a 32nd of the keys, which all of them hold in LDS.
-// The workgroups from z.first on clear the gradient meanwhile.
 __global__ __launch_bounds__(1024) void rank_kernel(const int64_t *tokens, int64_t vocab, int n, uint32_t *key_out,
-                                                   uint32_t *pos_out, ZeroArgs z) {
+                                                   uint32_t *pos_out) {
     __shared__ __align__(16) uint32_t keys[kRankMax];
     __shared__ int below[32][33];
-    if (int(blockIdx.x) >= z.first) {
-        fill_zero(z);
-        return;
-    }
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int padded = (n + 31) & ~31;
     {
@@ -234,15 +199,10 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, int64_t i) {
     return a.tokens ? key_of(a.tokens[i], a.vocab) : a.key[i];
 }
 
-// The first pass's workgroups from z.first on clear the gradient.
-__global__ __launch_bounds__(256) void sort_count_kernel(SortArgs a, ZeroArgs z) {
+__global__ __launch_bounds__(256) void sort_count_kernel(SortArgs a) {
     __shared__ uint32_t count[kSortBins];
     const int bins = 1 << a.bits;
-    if (int(blockIdx.x) >= z.first) {
-        fill_zero(z);
-        return;
-    }
-    for (int64_t b = blockIdx.x; b < a.blocks; b += z.first) {
+    for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
         for (int d = threadIdx.x; d < bins; d += 256)
             count[d] = 0;
         __syncthreads();
@@ -364,6 +324,7 @@ struct SumArgs {
     const uint32_t *key, *pos;  // sorted
     int32_t chunk;
     int64_t chunks;
+    int32_t workgroups;  // that take chunks; those behind them clear rows
     float *part;  // [chunk][2][dim]: of a run from before, of one that starts here and goes on
 };
 
@@ -389,6 +350,120 @@ __device__ __forceinline__ void write_row(const RowsArgs &r, uint32_t row, const
     }
 }
 
+// Few tokens, without a sort: a workgroup takes a position at its lanes' columns,
+// looks for its token among all positions, 64 a ballot, leaves if one before it
+// has the same, and else sums the rows of those that have it in their order, a
+// quarter by each of its 4 waves.
+template <typename T, int P, bool kAdd>
+__global__ __launch_bounds__(256) void few_kernel(RowsArgs r) {
+    __shared__ uint16_t list[kFewTokens];
+    __shared__ Some<P> red[3][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Columns<P> c((int64_t(blockIdx.y) * 64 + lane) * P, r.dim);
+    const T *x = static_cast<const T *>(r.x) + c.at;
+    const int n = int(r.n);
+    int64_t tokens[kFewTokens / 64];
+#pragma unroll
+    for (int k = 0; k < kFewTokens / 64; ++k)
+        tokens[k] = k * 64 + lane < n ? r.tokens[k * 64 + lane] : -1;
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const int64_t token = r.tokens[i];
+        if (token < 0 || token >= r.vocab)
+            continue;
+        int total = 0;
+        bool first = true;
+#pragma unroll
+        for (int k = 0; k < kFewTokens / 64; ++k) {
+            const int j = k * 64 + lane;
+            const bool same = tokens[k] == token;
+            const uint64_t all = __ballot(same);
+            first = first && !__any(same && j < i);
+            if (same)
+                list[total + __popcll(all & ((uint64_t(1) << lane) - 1))] = uint16_t(j);   // by each wave alike
+            total += __popcll(all);
+        }
+        if (!first)
+            continue;
+        __syncthreads();
+        const int to = total * (wave + 1) / 4;
+        Some<P> e{};
+        if (c.any) {
+            int k = total * wave / 4;
+            for (; k + 8 <= to; k += 8) {
+                Some<P> v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = load_some<P>(x + int64_t(list[k + u]) * r.stride);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    add(e, v[u]);
+            }
+            for (; k < to; ++k)
+                add(e, load_some<P>(x + int64_t(list[k]) * r.stride));
+        }
+        if (wave < 3)
+            red[wave][lane] = e;
+        __syncthreads();
+        if (wave == 3 && c.any) {   // the last quarter is never empty
+            Some<P> sum = red[0][lane];
+            add(sum, red[1][lane]);
+            add(sum, red[2][lane]);
+            add(sum, e);
+            write_row<kAdd>(r, uint32_t(token), c, sum);
+        }
+        __syncthreads();
+    }
+}
+
+// The first of key[from, to) that is not below `limit`: all 64 lanes probe.
+__device__ __forceinline__ int64_t first_not_below(const uint32_t *key, int64_t from, int64_t to, uint32_t limit) {
+    const int lane = threadIdx.x & 63;
+    while (from < to) {
+        const int64_t step = (to - from + 63) / 64, probe = from + (lane + 1) * step - 1;
+        const int below = __popcll(__ballot(probe < to && key[probe] < limit));
+        from += below * step;
+        to = to < from + step - 1 ? to : from + step - 1;
+    }
+    return to;
+}
+
+// Clears the rows of the parameter that no token names, those behind the
+// vocabulary among them, 64 a workgroup: lane l looks for row l among the keys.
+// Beside the sums, for both wait for memory in different ways (8,192 tokens of
+// GPT-2 small 34.6 us, 37.2 with all rows cleared beside the sort; Llama-3-8B,
+// bound by writing a gigabyte, 232 and 228; every 2004th row a workgroup, so that
+// all write one region together, 249).
+constexpr int kClearRows = 64;
+
+template <int P>
+__device__ __forceinline__ void clear_unnamed(const SumArgs &a, const Columns<P> &c) {
+    const RowsArgs &r = a.r;
+    const int64_t rows = r.numel / r.dim, groups = (rows + kClearRows - 1) / kClearRows;
+    for (int64_t g = blockIdx.x - a.workgroups; g < groups; g += gridDim.x - a.workgroups) {
+        const int64_t row0 = g * kClearRows, row = row0 + (threadIdx.x & 63);
+        const int64_t behind = row0 + kClearRows < r.vocab ? row0 + kClearRows : r.vocab;
+        int64_t lo = r.n, end = r.n;
+        if (row0 < r.vocab) {
+            lo = first_not_below(a.key, 0, r.n, uint32_t(row0));
+            end = first_not_below(a.key, lo, r.n, uint32_t(behind));
+        }
+        for (int64_t hi = end; lo < hi;) {
+            const int64_t mid = (lo + hi) / 2;
+            if (a.key[mid] < uint32_t(row))
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        const bool named = lo < end && a.key[lo] == uint32_t(row);
+        for (uint64_t left = __ballot(row < rows && !named); left; left &= left - 1)
+            if (c.any)
+                store_some(r.g + (row0 + __builtin_ctzll(left)) * r.dim + c.at, Some<P>{});
+        if (g == groups - 1 && blockIdx.y == 0)
+            for (int64_t i = rows * r.dim + threadIdx.x; i < r.numel; i += blockDim.x)
+                r.g[i] = 0;
+    }
+}
+
 template <typename T, int P, bool kAdd, bool kOnce>
 __global__ __launch_bounds__(256) void runs_kernel(SumArgs a) {
     const RowsArgs &r = a.r;
@@ -396,7 +471,11 @@ __global__ __launch_bounds__(256) void runs_kernel(SumArgs a) {
     const Columns<P> c((int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * P, r.dim);
     const T *x = static_cast<const T *>(r.x) + c.at;
     const uint32_t none = uint32_t(r.vocab);
-    for (int64_t b = blockIdx.x; b < a.chunks; b += gridDim.x) {
+    if (!kAdd && int(blockIdx.x) >= a.workgroups) {
+        clear_unnamed(a, c);
+        return;
+    }
+    for (int64_t b = blockIdx.x; b < a.chunks; b += a.workgroups) {
         const int64_t i0 = b * a.chunk;
         const int in = r.n - i0 < a.chunk ? int(r.n - i0) : a.chunk;
         const uint32_t my_key = lane < in ? a.key[i0 + lane] : none, my_pos = lane < in ? a.pos[i0 + lane] : 0u;
@@ -495,6 +574,22 @@ __global__ __launch_bounds__(256) void join_kernel(SumArgs a) {
     }
 }
 
+// Few workgroups clear faster than many: 1 GB by 256 in 160 us, by 512 in 195, by
+// 4096 in 232, non-temporally in 166 to 264.
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
+    const int64_t head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / 2, from = head < n ? head : n;
+    const int64_t chunks = (n - from) / 8, upto = from + chunks * 8;
+    if (blockIdx.x == 0) {
+        if (int64_t(threadIdx.x) < from)
+            p[threadIdx.x] = 0;
+        if (upto + threadIdx.x < n)
+            p[upto + threadIdx.x] = 0;
+    }
+    u32x4 *q = reinterpret_cast<u32x4 *>(p + from);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256)
+        q[i] = u32x4{0, 0, 0, 0};
+}
+
 // ---- around the cross entropy's products --------------------------------------------------------
 
 // Rows of dim elements, one every `stride`, to `padded` rows of kdim, zeros
@@ -585,11 +680,6 @@ __global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum,
 
 unsigned grid_of(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, std::min<int64_t>(kMaxGrid, 1 << 20))); }
 
-// Workgroups that clear n elements.
-unsigned zero_grid(int64_t n) {
-    return unsigned(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 8 * kZeroThreads), grid_of(kZeroGroups))));
-}
-
 void pack(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim, int64_t kdim, int64_t padded,
           const int64_t *targets, int64_t vocab, uint16_t *to, hipStream_t stream) {
     pack_kernel<<<grid_of(ceil_div(padded * kdim, 2048)), 256, 0, stream>>>(from, stride, rows, dim, kdim, padded,
@@ -618,7 +708,7 @@ const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64
 
 hipError_t launch_zero(uint16_t *p, int64_t n, hipStream_t stream) {
     if (n > 0)
-        zero_kernel<<<zero_grid(n), kZeroThreads, 0, stream>>>(ZeroArgs{p, n, 0});
+        zero_kernel<<<grid_of(std::min<int64_t>(256, ceil_div(n, 2048))), 256, 0, stream>>>(p, n);
     return hipGetLastError();
 }
 
@@ -637,10 +727,11 @@ hipError_t launch_lookup(const LookupArgs &a, hipStream_t stream) {
 
 // The sums of rows, P columns a lane.
 template <typename T, int P, bool kAdd>
-void launch_sums(const SumArgs &s, hipStream_t stream) {
+void launch_sums(SumArgs s, hipStream_t stream) {
     const int64_t waves = std::min<int64_t>(4, ceil_div(s.r.dim, 64 * P));
-    const unsigned chunks = grid_of(s.chunks);
-    const dim3 grid(chunks, unsigned(ceil_div(s.r.dim, 64 * P * waves)));
+    s.workgroups = int32_t(grid_of(s.chunks));
+    const unsigned clear = kAdd ? 0 : grid_of(ceil_div(s.r.numel / s.r.dim, kClearRows));
+    const dim3 grid(unsigned(s.workgroups) + clear, unsigned(ceil_div(s.r.dim, 64 * P * waves)));
     // rows that the 256 MB Infinity Cache can hold are mostly still in it
     // (GPT-2 small's 12 MB: 8.2 us, 10.0 non-temporally); more are not (537 MB:
     // 121 us, 101 non-temporally)
@@ -650,22 +741,37 @@ void launch_sums(const SumArgs &s, hipStream_t stream) {
         runs_kernel<T, P, kAdd, false><<<grid, unsigned(64 * waves), 0, stream>>>(s);
     if (s.chunks > 1) {
         constexpr int J = P == 1 ? 1 : 4;   // of fp32
-        join_kernel<J, kAdd><<<dim3(chunks, unsigned(ceil_div(s.r.dim, 64 * J))), 256, 0, stream>>>(s);
+        join_kernel<J, kAdd><<<dim3(unsigned(s.workgroups), unsigned(ceil_div(s.r.dim, 64 * J))), 256, 0, stream>>>(s);
     }
 }
 
 hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return a.accumulate ? hipSuccess : launch_zero(a.g, a.numel, stream);
+    auto one_of = [&](auto f32, auto bf16, auto f32_add, auto bf16_add) {
+        return a.accumulate ? (a.f32 ? f32_add : bf16_add) : (a.f32 ? f32 : bf16);
+    };
+    if (a.n <= kFewTokens) {
+        if (!a.accumulate)
+            if (hipError_t e = launch_zero(a.g, a.numel, stream); e != hipSuccess)
+                return e;
+        const int P = a.dim < 8 ? 1 : a.f32 ? 4 : 8;
+        const dim3 grid(grid_of(a.n), unsigned(ceil_div(a.dim, 64 * P)));
+        if (P == 1)
+            one_of(few_kernel<float, 1, false>, few_kernel<uint16_t, 1, false>, few_kernel<float, 1, true>,
+                   few_kernel<uint16_t, 1, true>)<<<grid, 256, 0, stream>>>(a);
+        else
+            one_of(few_kernel<float, 4, false>, few_kernel<uint16_t, 8, false>, few_kernel<float, 4, true>,
+                   few_kernel<uint16_t, 8, true>)<<<grid, 256, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     const RowsLayout l = rows_layout(a.n, a.dim);
     char *ws = static_cast<char *>(a.workspace);
     auto u32 = [&](int64_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
     int set = 0;
     if (a.n <= kRankMax) {
-        const unsigned blocks = unsigned(ceil_div(a.n, 32));
-        const ZeroArgs z{a.g, a.numel, int32_t(blocks)};
-        rank_kernel<<<blocks + (a.accumulate ? 0 : zero_grid(a.numel)), 1024, 0, stream>>>(
-            a.tokens, a.vocab, int(a.n), u32(l.key[0]), u32(l.pos[0]), z);
+        rank_kernel<<<unsigned(ceil_div(a.n, 32)), 1024, 0, stream>>>(a.tokens, a.vocab, int(a.n), u32(l.key[0]),
+                                                                     u32(l.pos[0]));
     } else {
         const int bits = 64 - __builtin_clzll(uint64_t(a.vocab)), passes = (bits + 8) / 9;
         const int digit = (bits + passes - 1) / passes;
@@ -684,9 +790,7 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
             p.key_out = u32(l.key[set]);
             p.pos_out = u32(l.pos[set]);
             p.shift = k * digit;
-            const unsigned count = grid_of(l.blocks);
-            sort_count_kernel<<<count + (k || a.accumulate ? 0 : zero_grid(a.numel)), 256, 0, stream>>>(
-                p, ZeroArgs{a.g, a.numel, int32_t(count)});
+            sort_count_kernel<<<grid_of(l.blocks), 256, 0, stream>>>(p);
             sort_scan_kernel<<<unsigned(ceil_div(int64_t(1) << digit, 4)), 256, 0, stream>>>(p);
             sort_move_kernel<<<grid_of(l.blocks), 256, 0, stream>>>(p);
         }
@@ -698,13 +802,12 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
     s.chunk = l.chunk;
     s.chunks = l.chunks;
     s.part = reinterpret_cast<float *>(ws + l.part);
-    auto go = [&](auto f32, auto bf16) { (a.f32 ? f32 : bf16)(s, stream); };
-    if (a.accumulate)
-        a.dim >= 8 ? go(launch_sums<float, 4, true>, launch_sums<uint16_t, 8, true>)
-                   : go(launch_sums<float, 1, true>, launch_sums<uint16_t, 1, true>);
+    if (a.dim < 8)
+        one_of(launch_sums<float, 1, false>, launch_sums<uint16_t, 1, false>, launch_sums<float, 1, true>,
+               launch_sums<uint16_t, 1, true>)(s, stream);
     else
-        a.dim >= 8 ? go(launch_sums<float, 4, false>, launch_sums<uint16_t, 8, false>)
-                   : go(launch_sums<float, 1, false>, launch_sums<uint16_t, 1, false>);
+        one_of(launch_sums<float, 4, false>, launch_sums<uint16_t, 8, false>, launch_sums<float, 4, true>,
+               launch_sums<uint16_t, 8, true>)(s, stream);
     return hipGetLastError();
 }
 
