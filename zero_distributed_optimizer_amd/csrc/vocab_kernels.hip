@@ -592,28 +592,39 @@ __global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
 
 // ---- around the cross entropy's products --------------------------------------------------------
 
-// Rows of dim elements, one every `stride`, to `padded` rows of kdim, zeros
-// behind the elements and the rows, and where targets (if given) names no row.
-__global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim,
-                                                  int64_t kdim, int64_t padded, const int64_t *targets,
-                                                  int64_t vocab, uint16_t *to) {
-    const int64_t per = kdim / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < padded * per; i += int64_t(gridDim.x) * 256) {
+// Rows of dim elements, one every `stride`, to `padded` rows of kdim, zeros behind
+// the elements and the rows, and where targets (if given) names no row; `copies`
+// times, one behind the other.
+struct Pack {
+    const uint16_t *from;
+    int64_t stride, rows, padded;
+    const int64_t *targets;
+    uint16_t *to;
+    int32_t copies, workgroups;
+};
+
+// Two packings in one launch (the second may be empty).
+__global__ __launch_bounds__(256) void pack_kernel(Pack one, Pack two, int64_t dim, int64_t kdim, int64_t vocab) {
+    const bool second = int(blockIdx.x) >= one.workgroups;
+    const Pack p = second ? two : one;
+    const int64_t per = kdim / 8, first = blockIdx.x - (second ? one.workgroups : 0);
+    for (int64_t i = first * 256 + threadIdx.x; i < p.padded * per; i += int64_t(p.workgroups) * 256) {
         const int64_t r = i / per, c = i % per * 8;
-        const uint16_t *p = from + r * stride + c;
-        bool keep = r < rows;
-        if (keep && targets) {
-            const int64_t target = targets[r];
+        const uint16_t *from = p.from + r * p.stride + c;
+        bool keep = r < p.rows;
+        if (keep && p.targets) {
+            const int64_t target = p.targets[r];
             keep = target >= 0 && target < vocab;
         }
         u32x4 x = {0, 0, 0, 0};
         if (keep && c + 8 <= dim)
-            x = *reinterpret_cast<const loose_u32x4 *>(p);
+            x = *reinterpret_cast<const loose_u32x4 *>(from);
         else if (keep)
             for (int k = 0; k < 7; ++k)
                 if (c + k < dim)
-                    x[k >> 1] |= uint32_t(p[k]) << (k & 1) * 16;
-        *reinterpret_cast<u32x4 *>(to + r * kdim + c) = x;
+                    x[k >> 1] |= uint32_t(from[k]) << (k & 1) * 16;
+        for (int copy = 0; copy < p.copies; ++copy)
+            *reinterpret_cast<u32x4 *>(p.to + (copy * p.padded + r) * kdim + c) = x;
     }
 }
 
@@ -680,10 +691,12 @@ __global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum,
 
 unsigned grid_of(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, std::min<int64_t>(kMaxGrid, 1 << 20))); }
 
-void pack(const uint16_t *from, int64_t stride, int64_t rows, int64_t dim, int64_t kdim, int64_t padded,
-          const int64_t *targets, int64_t vocab, uint16_t *to, hipStream_t stream) {
-    pack_kernel<<<grid_of(ceil_div(padded * kdim, 2048)), 256, 0, stream>>>(from, stride, rows, dim, kdim, padded,
-                                                                           targets, vocab, to);
+// The packings that a product needs, in one launch if there are any.
+void launch_pack(Pack one, Pack two, const CeArgs &a, const CeLayout &l, hipStream_t stream) {
+    for (Pack *p : {&one, &two})
+        p->workgroups = int32_t(grid_of(ceil_div(p->padded * l.kdim, 2048)));
+    if (one.workgroups + two.workgroups > 0)
+        pack_kernel<<<unsigned(one.workgroups + two.workgroups), 256, 0, stream>>>(one, two, a.dim, l.kdim, a.vocab);
 }
 
 // W where it lies serves the products if its rows are whole steps and 16-byte
@@ -696,11 +709,14 @@ bool in_place(const CeArgs &a) { return a.dim % kDepth == 0 && (reinterpret_cast
 // the products are as fast: 184 and 182, GPT-2 small 23.5 and 21.8).
 bool by_rows(const CeArgs &a) { return a.n <= kThinTokens && !in_place(a); }
 
-const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64_t rows, hipStream_t stream) {
+// A piece of W as the products take it: in place, or the copy that `p` describes.
+const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64_t rows, Pack &p) {
+    p = Pack{};
+    const uint16_t *from = a.w + row0 * a.dim;
     if (in_place(a))
-        return a.w + row0 * a.dim;
+        return from;
     uint16_t *w = reinterpret_cast<uint16_t *>(a.workspace + l.w);
-    pack(a.w + row0 * a.dim, a.dim, rows, a.dim, l.kdim, rows, nullptr, 0, w, stream);
+    p = Pack{from, a.dim, rows, rows, nullptr, w, 1, 0};
     return w;
 }
 
@@ -834,9 +850,10 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
             return e;
         tiles = ceil_div(g.m, kThinRows);
     } else {
+        Pack hidden{}, w;
         if (a.dim % kDepth || g.ldb % 8 || g.ldb > int64_t(1) << 21 || (reinterpret_cast<uintptr_t>(a.hidden) & 15)) {
             uint16_t *h = reinterpret_cast<uint16_t *>(a.workspace + l.hidden);
-            pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, a.n, nullptr, 0, h, stream);
+            hidden = Pack{a.hidden, a.hidden_stride, a.n, a.n, nullptr, h, 1, 0};
             g.b = h;
             g.ldb = l.kdim;
         }
@@ -846,7 +863,9 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
         const int64_t rows = in_place(a) ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
         for (g.row0 = 0; g.row0 < a.vocab; g.row0 += rows) {
             g.m = std::min(rows, a.vocab - g.row0);
-            g.a = piece_of(a, l, g.row0, g.m, stream);
+            g.a = piece_of(a, l, g.row0, g.m, w);
+            launch_pack(hidden, w, a, l, stream);
+            hidden = Pack{};
             g.tile0 = tiles;
             if (hipError_t e = launch_gemm(kScore, g, stream); e != hipSuccess)
                 return e;
@@ -874,13 +893,13 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     uint16_t *hidden = u16(l.hidden), *d = u16(l.d);
     float *sum = reinterpret_cast<float *>(a.workspace + l.sum);
     // hidden with zeros where no target is: whatever those rows hold, nothing of it is left
-    for (int64_t part = 0; part < (a.grads ? l.parts : 1); ++part)
-        pack(a.hidden, a.hidden_stride, a.n, a.dim, l.kdim, l.npad, a.targets, a.vocab,
-             hidden + part * l.npad * l.kdim, stream);
+    Pack packed{a.hidden, a.hidden_stride, a.n, l.npad, a.targets, hidden, int32_t(a.grads ? l.parts : 1), 0}, piece;
     float *rest = reinterpret_cast<float *>(a.workspace + l.rest);
     for (int64_t row0 = 0; row0 < a.vocab; row0 += l.piece) {
         const int64_t rows = std::min(l.piece, a.vocab - row0);
-        const uint16_t *w = piece_of(a, l, row0, rows, stream);
+        const uint16_t *w = piece_of(a, l, row0, rows, piece);
+        launch_pack(packed, piece, a, l, stream);
+        packed = Pack{};
         GemmArgs g{};
         g.a = w;
         g.b = hidden;
