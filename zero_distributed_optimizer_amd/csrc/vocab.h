@@ -53,7 +53,7 @@ struct RowsArgs {
 };
 
 // Up to this many positions are not sorted at all (see few_kernel: 300 tokens of 250
-// columns 6.8 us, 13 by the sort; a token that all of them name is summed in 16
+// columns 5.0 us, 13 by the sort; a token that all of them name is summed in 16
 // rounds of loads).
 constexpr int64_t kFewTokens = 512;
 

@@ -353,11 +353,13 @@ __device__ __forceinline__ void write_row(const RowsArgs &r, uint32_t row, const
 // Few tokens, without a sort: a workgroup takes a position at its lanes' columns,
 // looks for its token among all positions, 64 a ballot, leaves if one before it
 // has the same, and else sums the rows of those that have it in their order, a
-// quarter by each of its 4 waves.
+// quarter by each of its 4 waves. The workgroups behind the first `workgroups`
+// clear the rows that no token names, 64 each, a row a wave.
 template <typename T, int P, bool kAdd>
-__global__ __launch_bounds__(256) void few_kernel(RowsArgs r) {
+__global__ __launch_bounds__(256) void few_kernel(RowsArgs r, int workgroups) {
     __shared__ uint16_t list[kFewTokens];
     __shared__ Some<P> red[3][64];
+    __shared__ uint32_t is_named[64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Columns<P> c((int64_t(blockIdx.y) * 64 + lane) * P, r.dim);
     const T *x = static_cast<const T *>(r.x) + c.at;
@@ -366,7 +368,28 @@ __global__ __launch_bounds__(256) void few_kernel(RowsArgs r) {
 #pragma unroll
     for (int k = 0; k < kFewTokens / 64; ++k)
         tokens[k] = k * 64 + lane < n ? r.tokens[k * 64 + lane] : -1;
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    if (!kAdd && int(blockIdx.x) >= workgroups) {
+        const int64_t rows = r.numel / r.dim, groups = (rows + 63) / 64;
+        for (int64_t g = blockIdx.x - workgroups; g < groups; g += gridDim.x - workgroups) {
+            if (threadIdx.x < 64)
+                is_named[threadIdx.x] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kFewTokens / 64; ++k)
+                if (tokens[k] >= g * 64 && tokens[k] < g * 64 + 64 && tokens[k] < r.vocab)
+                    is_named[tokens[k] - g * 64] = 1;   // by whoever has it
+            __syncthreads();
+            for (int k = wave; k < 64 && g * 64 + k < rows; k += 4)
+                if (!is_named[k] && c.any)
+                    store_some(r.g + (g * 64 + k) * r.dim + c.at, Some<P>{});
+            if (g == groups - 1 && blockIdx.y == 0)
+                for (int64_t i = rows * r.dim + threadIdx.x; i < r.numel; i += 256)
+                    r.g[i] = 0;
+            __syncthreads();
+        }
+        return;
+    }
+    for (int i = blockIdx.x; i < n; i += workgroups) {
         const int64_t token = r.tokens[i];
         if (token < 0 || token >= r.vocab)
             continue;
@@ -768,17 +791,15 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
         return a.accumulate ? (a.f32 ? f32_add : bf16_add) : (a.f32 ? f32 : bf16);
     };
     if (a.n <= kFewTokens) {
-        if (!a.accumulate)
-            if (hipError_t e = launch_zero(a.g, a.numel, stream); e != hipSuccess)
-                return e;
-        const int P = a.dim < 8 ? 1 : a.f32 ? 4 : 8;
-        const dim3 grid(grid_of(a.n), unsigned(ceil_div(a.dim, 64 * P)));
+        const int P = a.dim < 8 ? 1 : a.f32 ? 4 : 8, workgroups = int(grid_of(a.n));
+        const dim3 grid(unsigned(workgroups) + (a.accumulate ? 0 : grid_of(ceil_div(a.numel / a.dim, 64))),
+                        unsigned(ceil_div(a.dim, 64 * P)));
         if (P == 1)
             one_of(few_kernel<float, 1, false>, few_kernel<uint16_t, 1, false>, few_kernel<float, 1, true>,
-                   few_kernel<uint16_t, 1, true>)<<<grid, 256, 0, stream>>>(a);
+                   few_kernel<uint16_t, 1, true>)<<<grid, 256, 0, stream>>>(a, workgroups);
         else
             one_of(few_kernel<float, 4, false>, few_kernel<uint16_t, 8, false>, few_kernel<float, 4, true>,
-                   few_kernel<uint16_t, 8, true>)<<<grid, 256, 0, stream>>>(a);
+                   few_kernel<uint16_t, 8, true>)<<<grid, 256, 0, stream>>>(a, workgroups);
         return hipGetLastError();
     }
     const RowsLayout l = rows_layout(a.n, a.dim);
