@@ -33,13 +33,14 @@
  *     without a contribution become 0); otherwise the gradient is added to
  *     what is there, in fp32 and rounded once, and embedding_grad leaves rows
  *     that no token names as they were.
- *   - n is in [0, 2^30], vocab in [1, 2^30], dim in [1, 2^20]; with n = 0 the
- *     gradients are those of no tokens, and the token arrays may be NULL.
+ *   - n is in [0, 2^30] (the loss: [0, 2^22]), vocab in [1, 2^30], dim in
+ *     [1, 2^20], strides at most 2^30; with n = 0 the gradients are those of no tokens, and the token arrays may be NULL.
  *   - workspace: device memory, 16-byte aligned, as many bytes as the call's
  *     query says, this call's alone until it completes. Two graphs that may
  *     run at the same time need two.
- *   - Results depend on the inputs and sizes only, bit for bit: sums have a
- *     fixed order, and no result goes through an atomic addition.
+ *   - Equal calls give equal bits: sums have a fixed order, which depends on the
+ *     sizes and on where W starts and how long its rows are, and no result goes
+ *     through an atomic addition.
  */
 #ifndef ZDO_VOCAB_H
 #define ZDO_VOCAB_H
@@ -65,11 +66,11 @@ int embedding_lookup(const zdo_plan *plan, int32_t param_index, int64_t vocab, i
 int64_t zdo_embedding_grad_workspace_bytes(int64_t n, int64_t dim);
 
 /* The lookup's gradient: for every row v, scale * (the sum of grad_out_i over
- * the tokens i that name v), added in fp32 in the tokens' order (long runs of
- * a token in pieces of fixed length), multiplied by scale and rounded once
- * to bf16, into the parameter's elements of grads. The positions are sorted by
- * token on the device; no two rows are written by the same thread, so equal
- * tokens need no atomics. grads and workspace must not overlap the inputs or
+ * the tokens i that name v), added in fp32 in the tokens' order (in pieces, whose
+ * sums are then added in order), multiplied by scale and rounded once to bf16,
+ * into the parameter's elements of grads. The positions are sorted by token on
+ * the device, so that a row is summed without atomics however many tokens name
+ * it. grads and workspace must not overlap the inputs or
  * each other. */
 int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim, const int64_t *tokens,
                    int64_t n, const void *grad_out, int32_t grad_type, int64_t grad_stride, float scale,
@@ -77,7 +78,10 @@ int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int
 
 /* Workspace bytes linear_cross_entropy and linear_cross_entropy_grad need (the
  * same for both, so that one workspace serves a step); -1 for sizes out of
- * range. It grows with n + vocab, not with their product. */
+ * range (n here is at most 2^22, and so it is in both calls). It is about n *
+ * dim elements of hidden and of grad_hidden's fp32 sum, and at most 256 MB each
+ * (or 512 bytes a token) of one piece's d and, where W is copied, of its rows: it
+ * does not grow with n * vocab. */
 int64_t zdo_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
 
 /* Softmax cross entropy of the logits z_i = W hidden_i, which are never kept:
