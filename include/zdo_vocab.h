@@ -34,7 +34,8 @@
  *     what is there, in fp32 and rounded once, and embedding_grad leaves rows
  *     that no token names as they were.
  *   - n is in [0, 2^30] (the loss: [0, 2^22]), vocab in [1, 2^30], dim in
- *     [1, 2^20], strides at most 2^30; with n = 0 the gradients are those of no tokens, and the token arrays may be NULL.
+ *     [1, 2^20], strides at most 2^30; with n = 0 the gradients are those of no
+ *     tokens, and the token arrays may be NULL.
  *   - workspace: device memory, 16-byte aligned, as many bytes as the call's
  *     query says, this call's alone until it completes. Two graphs that may
  *     run at the same time need two.
@@ -68,20 +69,19 @@ int64_t zdo_embedding_grad_workspace_bytes(int64_t n, int64_t dim);
 /* The lookup's gradient: for every row v, scale * (the sum of grad_out_i over
  * the tokens i that name v), added in fp32 in the tokens' order (in pieces, whose
  * sums are then added in order), multiplied by scale and rounded once to bf16,
- * into the parameter's elements of grads. The positions are sorted by token on
- * the device, so that a row is summed without atomics however many tokens name
- * it. grads and workspace must not overlap the inputs or
- * each other. */
+ * into the parameter's elements of grads. The device orders the positions by
+ * token, so that a row is summed without atomics however many tokens name it. grads and workspace must not overlap the inputs or each other. */
 int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim, const int64_t *tokens,
                    int64_t n, const void *grad_out, int32_t grad_type, int64_t grad_stride, float scale,
                    int32_t accumulate, uint16_t *grads, void *workspace, void *stream);
 
 /* Workspace bytes linear_cross_entropy and linear_cross_entropy_grad need (the
  * same for both, so that one workspace serves a step); -1 for sizes out of
- * range (n here is at most 2^22, and so it is in both calls). It is about n *
- * dim elements of hidden and of grad_hidden's fp32 sum, and at most 256 MB each
- * (or 512 bytes a token) of one piece's d and, where W is copied, of its rows: it
- * does not grow with n * vocab. */
+ * range (n here is at most 2^22, and so it is in both calls). It holds hidden in
+ * bf16 and, for the gradient, its sum in fp32; a piece's d and its rows of W, at
+ * most 256 MB each (or 512 bytes a token, and for each of dim); the sums of
+ * splits, at most 128 MB for each gradient; for the loss, in the place of d and the
+ * sums, 8 bytes for each token and 128 rows of W (64 for up to 32 tokens). */
 int64_t zdo_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
 
 /* Softmax cross entropy of the logits z_i = W hidden_i, which are never kept:
@@ -102,9 +102,10 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
  * two products, as their results are, and the products' sums are in fp32; what
  * the rounding leaves of d_i[targets_i], the largest term of most sums, is added
  * to grad_hidden in fp32, and for up to 128 tokens W's gradient takes d in two
- * bf16 parts. A token whose target names no row has a grad_hidden of zero. grad_hidden or grads may be NULL (not both): that gradient is not
- * computed. hidden's rows of tokens whose target names no row are not used.
- * Outputs and workspace must not overlap the inputs or each other. */
+ * bf16 parts. A token whose target names no row has a grad_hidden of zero.
+ * grad_hidden or grads may be NULL (not both): that gradient is not computed.
+ * hidden's rows of tokens whose target names no row are not used. Outputs
+ * and workspace must not overlap the inputs or each other. */
 int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,
                               const uint16_t *params, const uint16_t *hidden, int64_t hidden_stride,
                               const int64_t *targets, int64_t n, const float *lse, const float *grad_loss,

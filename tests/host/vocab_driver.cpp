@@ -120,7 +120,9 @@ static int layouts() {
         TRUE(256 * 2 * l.vpad < (int64_t(1) << 32) && 256 * 2 * l.kdim < (int64_t(1) << 32));
         TRUE(l.w - l.hidden >= 2 * l.parts * l.npad * l.kdim && l.d - l.w >= 2 * l.piece * l.kdim);
         TRUE(l.rest - l.d >= 2 * l.parts * l.npad * l.vpad && l.sum - l.rest >= 4 * n);
-        TRUE(l.bytes - l.sum >= 4 * l.splits * n * l.kdim);
+        TRUE(l.row_sum - l.sum >= 4 * l.splits * n * l.kdim);
+        TRUE(l.row_splits >= 1 && l.row_splits <= 1 + l.npad / 256);
+        TRUE(l.row_splits == 1 || l.bytes - l.row_sum >= 4 * l.row_splits * l.piece * l.kdim);
         // the loss's partial results: every launch's tiles, whatever their size
         int64_t tiles = 0;
         for (int64_t row = 0; row < vocab && tiles < 400000; row += l.piece)
@@ -138,7 +140,7 @@ static int layouts() {
         // products are numbered in 32 bits
         TRUE(ceil_div(dim, 128) * ceil_div(std::max<int64_t>(n, 1), 128) * l.splits <= (int64_t(1) << 30));
         TRUE(ceil_div(l.piece, 128) * ceil_div(std::max<int64_t>(n, 1), 128) <= (int64_t(1) << 30));
-        TRUE(ceil_div(dim, 128) * ceil_div(l.piece, 128) <= (int64_t(1) << 30));
+        TRUE(ceil_div(dim, 128) * ceil_div(l.piece, 128) * l.row_splits <= (int64_t(1) << 30));
 
         const int64_t m = t % 50 == 0 ? 0 : some(double(kVocabMaxN));
         const RowsLayout r = rows_layout(m, dim);

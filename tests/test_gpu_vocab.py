@@ -358,6 +358,19 @@ def test_cross_entropy(gpu, n, vocab, dim, before, pad, kind, how):
     check_ce(n, vocab, dim, before, pad, kind, how)
 
 
+# W's gradient is a few tiles, and its sum over the tokens is split
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab,dim,before,pad,kind,how", [
+    (4097, 300, 192, 0, 0, "zipf", "contiguous"),
+    (3001, 515, 65, 3, 2, "ends", "off"),
+    (2500, 1, 3, 0, 1, "uniform", "contiguous"),
+    (2049, 129, 1000, 8, 0, "zipf", "wide"),
+    (20000, 40, 7, 1, 0, "uniform", "off"),
+])
+def test_cross_entropy_of_few_rows(gpu, n, vocab, dim, before, pad, kind, how, accumulate):
+    check_ce(n, vocab, dim, before, pad, kind, how, accumulate=accumulate)
+
+
 @pytest.mark.parametrize("case", [4, 7, 8, 10, 11])
 @pytest.mark.parametrize("accumulate,dtype,parts", [(True, BF, "both"), (False, torch.float32, "hidden"),
                                                    (True, BF, "rows"), (True, torch.float32, "both")])
@@ -455,7 +468,8 @@ def test_embedding_by_64_workgroups(gpu, n, vocab, dim, kind):
         assert torch.equal(bits(a), bits(b))
 
 
-@pytest.mark.parametrize("n,vocab,dim,off", [(3000, 20000, 64, 0), (600, 20000, 100, 1), (16, 9000, 72, 1), (16, 9000, 64, 0)])
+@pytest.mark.parametrize("n,vocab,dim,off", [(3000, 20000, 64, 0), (600, 20000, 100, 1), (16, 9000, 72, 1), (16, 9000, 64, 0),
+                                             (5000, 1300, 136, 0)])
 def test_cross_entropy_by_64_workgroups(gpu, n, vocab, dim, off):
     sizes = ([off] if off else []) + [vocab * dim]
     total = sum(sizes) + 3

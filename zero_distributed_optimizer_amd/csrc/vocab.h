@@ -104,17 +104,17 @@ inline RowsLayout rows_layout(int64_t n, int64_t dim) {
 // kDepth elements, wide ones at least m or n up to a multiple of 8. Which is
 // which, and what becomes of C, is the epilogue's:
 //   kScore, kDiff: A and B long; kSum: A wide, B long (k of it up to a multiple
-//   of kDepth: zeros); kRows: A wide (with zero rows from k on, up to a multiple
-//   of kDepth), B wide (finite ones).
+//   of kDepth: zeros); kRows, kParts: A wide (with zero rows from k on, up to a
+//   multiple of kDepth), B wide (finite ones).
 constexpr int kDepth = 64;
 
-enum Epilogue : int { kScore, kDiff, kSum, kRows };
+enum Epilogue : int { kScore, kDiff, kSum, kRows, kParts };
 
 struct GemmArgs {
     const uint16_t *a, *b;
     int64_t lda, ldb;
     int64_t m, n, k;
-    int32_t splits;  // of k, each with an output of its own (kSum)
+    int32_t splits;  // of k, each with an output of its own (kSum, kParts)
 
     // kScore, kDiff: m are a piece's rows of W, n tokens
     const int64_t *targets;
@@ -133,7 +133,7 @@ struct GemmArgs {
     int64_t ldd;
     float *rest;
 
-    // kSum: fp32 [split][n][lds], added to what is there unless `first`
+    // kSum, kParts: fp32 [split][n][lds], added to what is there unless `first`
     float *sum;
     int64_t lds;
     int32_t first;
@@ -170,6 +170,28 @@ inline double product_us(int64_t m, int64_t n, int64_t k, int64_t splits) {
            (kRoundOwn + kRoundK * double(ceil_div(k, splits)));
 }
 
+// The splits of a product's k, of at least 256 and with at most 2^25 sums in all,
+// and the time with them: a sum and an addition take 8 bytes at 5 TB/s, and more
+// than one split `join` us. (A training pass whose W's gradient is split so, and in
+// one: 8,192 tokens of 256 rows of 768 77 us, 143; 16,384 of 300 rows of 512 86 and
+// 224; of GPT-2 small's 50,257, in smaller pieces, 5.00 ms and 5.52.)
+constexpr double kJoin = 4.0;
+struct Splits {
+    int64_t splits = 1;
+    double us = 0.0;
+};
+inline Splits splits_of(int64_t m, int64_t n, int64_t k, double join) {
+    Splits best{1, product_us(m, n, k, 1)};
+    const double each = join > 0.0 ? 0.0 : double(n * m) * 8 / 5e6;
+    best.us += each;
+    for (int64_t s = 2; s <= k / 256 && s * n * round_up(m, kDepth) <= int64_t(1) << 25; s += s < 4 ? 1 : s / 2) {
+        const double us = product_us(m, n, k, s) + join + double(s * n * m) * 8 / 5e6;
+        if (us < best.us)
+            best = {s, us};
+    }
+    return best;
+}
+
 // The loss of up to kThinTokens tokens may go by thin_score_kernel, kThinRows rows
 // of W a tile.
 constexpr int64_t kThinTokens = 32;
@@ -187,8 +209,9 @@ constexpr int64_t kTwoPartTokens = 128;
 struct CeLayout {
     int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
     int64_t splits;                   // of grad_hidden's sum
+    int64_t row_splits;               // of W's gradient's
     int64_t parts;                    // of d: 2 for few tokens
-    int64_t hidden, w, d, rest, sum, part, pick, bytes;
+    int64_t hidden, w, d, rest, sum, row_sum, part, pick, bytes;
 };
 
 inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
@@ -199,20 +222,19 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     int64_t most = std::min((int64_t(1) << 27) / l.npad, (int64_t(1) << 27) / l.kdim);
     most = std::max<int64_t>(256, most / 256 * 256);
     // the number of pieces, at least this many, and of splits of grad_hidden's sum
-    // over the vocabulary (each adds to an fp32 sum of its own at 5 TB/s)
+    // over the vocabulary (each adds to an fp32 sum of its own at 5 TB/s) and of W's
+    // gradient's over the tokens (which takes another launch to add them)
     const int64_t least = ceil_div(vocab, most);
     double best = 0.0;
     for (int64_t p = least; p < least + 4 && p <= vocab; ++p) {
         const int64_t piece = std::min(vocab, round_up(ceil_div(vocab, p), 256));
-        const double rest = product_us(piece, some, dim, 1) + product_us(dim, piece, some, 1);
-        for (int64_t s = 1; s == 1 || (s <= piece / 256 && s * some * l.kdim <= int64_t(1) << 25); s += s < 4 ? 1 : s / 2) {
-            const double us = double(ceil_div(vocab, piece)) *
-                              (rest + product_us(dim, some, piece, s) + double(s * some * dim) * 8 / 5e6);
-            if (best == 0.0 || us < best) {
-                best = us;
-                l.piece = piece;
-                l.splits = s;
-            }
+        const Splits sum = splits_of(dim, some, piece, 0.0), rows = splits_of(dim, piece, some, kJoin);
+        const double us = double(ceil_div(vocab, piece)) * (product_us(piece, some, dim, 1) + sum.us + rows.us);
+        if (best == 0.0 || us < best) {
+            best = us;
+            l.piece = piece;
+            l.splits = sum.splits;
+            l.row_splits = rows.splits;
         }
     }
     l.vpad = round_up(l.piece, kDepth);
@@ -236,6 +258,7 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     l.d = take(2 * l.parts * l.npad * l.vpad);
     l.rest = take(4 * n);
     l.sum = take(4 * l.splits * n * l.kdim);
+    l.row_sum = take(l.row_splits > 1 ? 4 * l.row_splits * l.piece * l.kdim : 0);
     l.bytes = std::max<int64_t>(std::max(at, loss), 256);
     return l;
 }

@@ -176,7 +176,7 @@ template <int BM, int BN, int WM, int WN, int E>
 __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WM * WN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles a wave
-    constexpr bool kWideA = E == kSum || E == kRows, kWideB = E == kRows;
+    constexpr bool kWideB = E == kRows || E == kParts, kWideA = E == kSum || kWideB;
     __shared__ __align__(1024) uint16_t stage[2][(BM + BN) * kDepth];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                             *reinterpret_cast<const u32x4 *>(&mine[n * PM + (c ^ (n & (CM - 1))) * 8]);
                 }
             }
-        } else if constexpr (E == kSum) {
+        } else if constexpr (E == kSum || E == kParts) {
             // rows of the sum are padded to kDepth, so quads never pass their end
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
@@ -667,6 +667,8 @@ hipError_t launch_gemm(Epilogue e, const GemmArgs &g, hipStream_t stream) {
         return launch_sized<kDiff>(g, stream);
     case kSum:
         return launch_sized<kSum>(g, stream);
+    case kParts:
+        return launch_sized<kParts>(g, stream);
     default:
         return launch_sized<kRows>(g, stream);
     }

@@ -712,6 +712,22 @@ __global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum,
     }
 }
 
+// The splits' sums of a piece of W's gradient, added in their order. Bound by
+// reading them, from the caches they were just written through.
+template <int P, bool kAdd>
+__global__ __launch_bounds__(256) void row_sums_kernel(RowsArgs r, const float *sum, int64_t splits, int64_t rows,
+                                                      int64_t kdim) {
+    const int64_t per = (r.dim + P - 1) / P;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / per;
+        const Columns<P> c(i % per * P, r.dim);
+        Some<P> e{};
+        for (int64_t s = 0; s < splits; ++s)
+            add(e, load_some<P, true>(sum + (s * rows + row) * kdim + c.at));
+        write_row<kAdd>(r, uint32_t(row), c, e);
+    }
+}
+
 unsigned grid_of(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, std::min<int64_t>(kMaxGrid, 1 << 20))); }
 
 // The packings that a product needs, in one launch if there are any.
@@ -966,11 +982,28 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
             r.m = a.dim;
             r.n = rows;
             r.k = l.parts * l.npad;
-            r.splits = 1;
+            r.splits = int32_t(l.row_splits);
             r.rows = a.grads + row0 * a.dim;
             r.accumulate = a.accumulate;
-            if (hipError_t e = launch_gemm(kRows, r, stream); e != hipSuccess)
+            r.sum = reinterpret_cast<float *>(a.workspace + l.row_sum);
+            r.lds = l.kdim;
+            r.first = 1;
+            if (hipError_t e = launch_gemm(l.row_splits > 1 ? kParts : kRows, r, stream); e != hipSuccess)
                 return e;
+            if (l.row_splits > 1) {
+                RowsArgs to{};
+                to.g = r.rows;
+                to.dim = a.dim;
+                to.scale = 1.0f;
+                auto go = [&](auto kernel) {
+                    kernel<<<grid_of(ceil_div(rows * l.kdim, 2048)), 256, 0, stream>>>(to, r.sum, l.row_splits, rows,
+                                                                                       l.kdim);
+                };
+                if (a.accumulate)
+                    a.dim >= 8 ? go(row_sums_kernel<8, true>) : go(row_sums_kernel<1, true>);
+                else
+                    a.dim >= 8 ? go(row_sums_kernel<8, false>) : go(row_sums_kernel<1, false>);
+            }
         }
     }
     if (a.grad_hidden) {
