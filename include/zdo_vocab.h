@@ -70,7 +70,8 @@ int64_t zdo_embedding_grad_workspace_bytes(int64_t n, int64_t dim);
  * the tokens i that name v), added in fp32 in the tokens' order (in pieces, whose
  * sums are then added in order), multiplied by scale and rounded once to bf16,
  * into the parameter's elements of grads. The device orders the positions by
- * token, so that a row is summed without atomics however many tokens name it. grads and workspace must not overlap the inputs or each other. */
+ * token, so that a row is summed without atomics however many tokens name it.
+ * grads and workspace must not overlap the inputs or each other. */
 int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim, const int64_t *tokens,
                    int64_t n, const void *grad_out, int32_t grad_type, int64_t grad_stride, float scale,
                    int32_t accumulate, uint16_t *grads, void *workspace, void *stream);
