@@ -204,10 +204,18 @@ constexpr int kThinRows = 64;
 // cancel, and its time is that of writing the gradient.
 constexpr int64_t kTwoPartTokens = 128;
 
+// Whether the products can read W where it lies: its rows are whole steps and
+// 16-byte aligned. Else they take a copy, piece by piece.
+inline bool rows_in_place(const void *w, int64_t dim) {
+    return dim % kDepth == 0 && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+}
+
 // A call's workspace. The vocabulary is taken in pieces of `piece` rows: at most
 // 2^27 elements of d (256 MB, the size of the Infinity Cache that they go
-// through to the two products that read them), but at least 256 rows, and at
-// most 2^27 elements of a copy of W.
+// through to the two products that read them), but at least 256 rows, and, unless
+// W is read in place, at most 2^27 elements of its copy (Llama-3-8B in
+// place, by the smaller pieces: a training pass of 64 tokens 1.17 ms, 1.35; of 1,024
+// 3.94 and 4.12).
 struct CeLayout {
     int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
     int64_t splits;                   // of grad_hidden's sum
@@ -216,19 +224,20 @@ struct CeLayout {
     int64_t hidden, w, d, rest, sum, row_sum, part, pick, bytes;
 };
 
-inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
+inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim, bool in_place) {
     CeLayout l{};
     const int64_t some = std::max<int64_t>(n, 1);
     l.kdim = round_up(dim, kDepth);
     l.npad = round_up(some, kDepth);
-    int64_t most = std::min((int64_t(1) << 27) / l.npad, (int64_t(1) << 27) / l.kdim);
+    int64_t most = (int64_t(1) << 27) / (in_place ? l.npad : std::max(l.npad, l.kdim));
     most = std::max<int64_t>(256, most / 256 * 256);
-    // the number of pieces, at least this many, and of splits of grad_hidden's sum
-    // over the vocabulary (each adds to an fp32 sum of its own at 5 TB/s) and of W's
-    // gradient's over the tokens (which takes another launch to add them)
-    const int64_t least = ceil_div(vocab, most);
+    // the number of pieces, at least this many (few tokens: no more, their tiles
+    // fill whole rounds anyway), and of splits of grad_hidden's sum over the
+    // vocabulary (each adds to an fp32 sum of its own at 5 TB/s) and of W's gradient's
+    // over the tokens (which takes another launch to add them)
+    const int64_t least = ceil_div(vocab, most), tries = n <= 512 ? 1 : 4;
     double best = 0.0;
-    for (int64_t p = least; p < least + 4 && p <= vocab; ++p) {
+    for (int64_t p = least; p < least + tries && p <= vocab; ++p) {
         const int64_t piece = std::min(vocab, round_up(ceil_div(vocab, p), 256));
         const Splits sum = splits_of(dim, some, piece, 0.0), rows = splits_of(dim, piece, some, kJoin);
         const double us = double(ceil_div(vocab, piece)) * (product_us(piece, some, dim, 1) + sum.us + rows.us);
@@ -248,11 +257,11 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     };
     l.parts = n <= kTwoPartTokens ? 2 : 1;
     l.hidden = take(2 * l.parts * l.npad * l.kdim);
-    l.w = take(2 * l.piece * l.kdim);
+    l.w = take(in_place ? 0 : 2 * l.piece * l.kdim);
     const int64_t both = at;
     // the loss
     const int64_t tiles = ceil_div(vocab, l.piece) * ceil_div(l.piece, kTileRowsMin);
-    l.part = take(8 * n * (n <= kThinTokens ? std::max(tiles, ceil_div(vocab, kThinRows)) : tiles));
+    l.part = take(8 * n * (n <= kThinTokens && !in_place ? std::max(tiles, ceil_div(vocab, kThinRows)) : tiles));
     l.pick = take(4 * n);
     const int64_t loss = at;
     // its gradient
@@ -265,9 +274,17 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim) {
     return l;
 }
 
+// What a caller provides, whether or not W will be read in place.
+inline int64_t ce_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
+    const int64_t copied = ce_layout(n, vocab, dim, false).bytes;
+    return dim % kDepth ? copied : std::max(copied, ce_layout(n, vocab, dim, true).bytes);
+}
+
 struct CeArgs {
     const uint16_t *w;  // row 0
     int64_t vocab, dim;
+    bool in_place;
+    CeLayout layout;
     const uint16_t *hidden;
     int64_t hidden_stride;
     const int64_t *targets;

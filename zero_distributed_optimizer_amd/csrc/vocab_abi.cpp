@@ -83,6 +83,18 @@ int check_rows(const void *p, int64_t n, int64_t dim, int64_t stride, int32_t ty
     return ZDO_OK;
 }
 
+// The cross entropy's arguments, as far as W and the number of tokens go.
+CeArgs args_at(const uint16_t *w, int64_t vocab, int64_t dim, int64_t n) {
+    CeArgs a{};
+    a.w = w;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.n = n;
+    a.in_place = rows_in_place(w, dim);
+    a.layout = ce_layout(n, vocab, dim, a.in_place);
+    return a;
+}
+
 Span span_of_rows(const void *p, int64_t n, int64_t dim, int64_t stride, int32_t type) {
     return span_of(p, n == 0 ? 0 : n == 1 ? dim : (n - 1) * stride + dim, bytes_of(type));
 }
@@ -189,7 +201,7 @@ int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int
 int64_t zdo_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
     if (!in_range(n, 0, kCeMaxN) || !in_range(vocab, 1, kVocabMaxRows) || !in_range(dim, 1, kVocabMaxDim))
         return -1;
-    return ce_layout(n, vocab, dim).bytes;
+    return ce_workspace_bytes(n, vocab, dim);
 }
 
 int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,
@@ -216,23 +228,19 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
             return rc;
         if (int rc = check_ptr(workspace, fn, "workspace"))
             return rc;
+        CeArgs a = args_at(params + w.start, vocab, dim, n);
         Buffers bufs;
         bufs.reads(span_of(params, plan->buffer_numel, 2), "params");
         bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, ZDO_BF16), "hidden");
         bufs.reads(span_of(targets, n, 8), "targets");
         bufs.writes(span_of(loss, n, 4), "loss");
         bufs.writes(span_of(lse, n, 4), "lse");
-        bufs.writes(span_of(workspace, ce_layout(n, vocab, dim).bytes, 1), "workspace");
+        bufs.writes(span_of(workspace, a.layout.bytes, 1), "workspace");
         if (int rc = bufs.check(fn))
             return rc;
-        CeArgs a{};
-        a.w = params + w.start;
-        a.vocab = vocab;
-        a.dim = dim;
         a.hidden = hidden;
         a.hidden_stride = hidden_stride;
         a.targets = targets;
-        a.n = n;
         a.loss = loss;
         a.lse = lse;
         a.workspace = static_cast<char *>(workspace);
@@ -277,6 +285,7 @@ int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t
                 return rc;
         if (int rc = check_ptr(workspace, fn, "workspace"))
             return rc;
+        CeArgs a = args_at(params + w.start, vocab, dim, n);
         Buffers bufs;
         bufs.reads(span_of(params, plan->buffer_numel, 2), "params");
         bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, ZDO_BF16), "hidden");
@@ -287,17 +296,12 @@ int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t
             bufs.writes(span_of_rows(grad_hidden, n, dim, grad_hidden_stride, grad_hidden_type), "grad_hidden");
         if (grads)
             bufs.writes(span_of(grads, plan->buffer_numel, 2), "grads");
-        bufs.writes(span_of(workspace, ce_layout(n, vocab, dim).bytes, 1), "workspace");
+        bufs.writes(span_of(workspace, a.layout.bytes, 1), "workspace");
         if (int rc = bufs.check(fn))
             return rc;
-        CeArgs a{};
-        a.w = params + w.start;
-        a.vocab = vocab;
-        a.dim = dim;
         a.hidden = hidden;
         a.hidden_stride = hidden_stride;
         a.targets = targets;
-        a.n = n;
         a.lse = const_cast<float *>(lse);   // read only by the gradient
         a.grad_loss = grad_loss;
         a.grad_hidden = grad_hidden;

@@ -357,6 +357,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
         } else if constexpr (E == kDiff) {
             // this wave's part of the tile, [n][m]
             constexpr int PM = BM / WM, PN = BN / WN;
+            // calls for d in two parts have one small tile along n (in large ones the
+            // second part's registers spill: 8,192 tokens of GPT-2 small 759 us, 724
+            // without it)
+            constexpr bool kLow = BM == kTileRowsMin;
             uint16_t *mine = reinterpret_cast<uint16_t *>(stage) + epi_wave * (PM * PN);
             uint32_t packed[4];
 #pragma unroll
@@ -395,12 +399,15 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float x = acc[i][j][2 * h] * weight, y = acc[i][j][2 * h + 1] * weight;
-                        const uint32_t high = to_bf16x2(x, y), low = to_bf16x2(x - lo_f32(high), y - hi_f32(high));
+                        const uint32_t high = to_bf16x2(x, y);
                         packed[h] = named ? high : 0u;
-                        packed[2 + h] = named ? low : 0u;
+                        if constexpr (kLow) {
+                            const uint32_t low = to_bf16x2(x - lo_f32(high), y - hi_f32(high));
+                            packed[2 + h] = named ? low : 0u;
+                        }
                     }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int r = 0; r < (kLow ? 4 : 2); ++r)
                         acc[i][j][r] = __uint_as_float(packed[r]);
                 }
             }
@@ -409,7 +416,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             constexpr int CM = PM / 8;
             const int pad_m = (rows_in + kDepth - 1) / kDepth * kDepth;
             const int pad_n = (cols_in + kDepth - 1) / kDepth * kDepth;
-            for (int part = 0; part < (g.low ? 2 : 1); ++part) {
+            for (int part = 0; part < (kLow && g.low ? 2 : 1); ++part) {
                 uint16_t *out = part ? g.low : g.d;
                 if (part)
                     __syncthreads();
@@ -450,28 +457,53 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                 }
             }
         } else {
+            // through LDS, in fp32, a wave's part [n][m] in as many passes as it
+            // takes, so that rows are written by 16 bytes a lane and 256 or 128
+            // bytes on end (Llama-3-8B's matrix from 64 tokens 447 us, 511 straight from
+            // registers by 8 bytes; from 4,096 3.55 and 3.62 ms). Quads are moved within
+            // their row by the row's number, so that the writes do not meet in a bank.
+            constexpr int PM = BM / WM, PN = BN / WN, CM = PM / 8;
+            constexpr int kPasses = BM * BN * 4 / int(sizeof(stage)), JN = TN / kPasses;
+            float *mine = reinterpret_cast<float *>(stage) + epi_wave * (PM * PN / kPasses);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int n = wave_n + j * 16 + lane_n;
-                uint16_t *row = g.rows + (n0 + n) * g.m + m0;
+            for (int pass = 0; pass < kPasses; ++pass) {
+                if (pass)
+                    __syncthreads();
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int m = wave_m + i * 16 + lane_m;
-                    if (n >= cols_in || m >= rows_in)
+                for (int j = 0; j < JN; ++j)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {
+                        const int n = j * 16 + lane_n, q = i * 4 + (epi_lane >> 4);
+                        *reinterpret_cast<f32x4 *>(&mine[n * PM + (q ^ (n & 15)) * 4]) = acc[i][pass * JN + j];
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < JN * 16 * CM / 64; ++i) {
+                    const int n = i * (64 / CM) + epi_lane / CM, c = epi_lane % CM;
+                    const int at_n = wave_n + pass * JN * 16 + n, at_m = wave_m + c * 8;
+                    if (at_n >= cols_in || at_m >= rows_in)
                         continue;
-                    f32x4 v = acc[i][j];
-                    if (m + 4 <= rows_in) {
-                        loose_u32x2 *at = reinterpret_cast<loose_u32x2 *>(row + m);
+                    const f32x4 lo = *reinterpret_cast<const f32x4 *>(&mine[n * PM + (2 * c ^ (n & 15)) * 4]);
+                    const f32x4 hi = *reinterpret_cast<const f32x4 *>(&mine[n * PM + ((2 * c + 1) ^ (n & 15)) * 4]);
+                    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    uint16_t *row = g.rows + (n0 + at_n) * g.m + m0 + at_m;
+                    if (at_m + 8 <= rows_in) {
+                        loose_u32x4 *to = reinterpret_cast<loose_u32x4 *>(row);
                         if (g.accumulate) {
-                            const u32x2 old = *at;
-                            v += f32x4{lo_f32(old.x), hi_f32(old.x), lo_f32(old.y), hi_f32(old.y)};
+                            const u32x4 old = *to;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                v[2 * r] += lo_f32(old[r]);
+                                v[2 * r + 1] += hi_f32(old[r]);
+                            }
                         }
-                        *at = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
+                        *to = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                                    to_bf16x2(v[6], v[7])};
                     } else {
-                        for (int r = 0; r < rows_in - m; ++r) {
-                            const float x = r == 0 ? v[0] : r == 1 ? v[1] : v[2];
-                            row[m + r] = uint16_t(to_bf16x2(g.accumulate ? x + h_f32(row[m + r]) : x, 0.0f));
-                        }
+#pragma unroll
+                        for (int r = 0; r < 7; ++r)
+                            if (at_m + r < rows_in)
+                                row[r] = uint16_t(to_bf16x2(g.accumulate ? v[r] + h_f32(row[r]) : v[r], 0.0f));
                     }
                 }
             }
@@ -636,18 +668,21 @@ __global__ __launch_bounds__(256, 2) void thin_score_kernel(GemmArgs g) {
 }
 
 // Workgroups of a launch: one a tile, up to a number whose threads fit 32
-// bits; more tiles are taken in turn.
+// bits; more tiles are taken in turn. For the logits and d in large tiles, one a
+// compute unit (8,192 tokens of GPT-2 small 588 and 700 us, 616 and 724 by one a
+// tile; sums and rows take the same or, of few tokens, 5% more).
 template <int BM, int BN, int WM, int WN, int E>
 hipError_t launch(const GemmArgs &g, hipStream_t stream) {
     const int64_t tiles = ceil_div(g.m, BM) * ceil_div(g.n, BN) * g.splits;
-    const int64_t cap = std::min<int64_t>(kMaxGrid, int64_t(1) << 21);
+    constexpr bool kStay = BM == 256 && (E == kScore || E == kDiff);
+    const int64_t cap = std::min<int64_t>(kMaxGrid, kStay ? 256 : 1 << 21);
     gemm_kernel<BM, BN, WM, WN, E><<<unsigned(std::min(tiles, cap)), WM * WN * 64, 0, stream>>>(g);
     return hipGetLastError();
 }
 
 template <int E>
 hipError_t launch_sized(const GemmArgs &g, hipStream_t stream) {
-    if (wide_tiles(g.m, g.n, g.splits))
+    if (E != kDiff || !g.low ? wide_tiles(g.m, g.n, g.splits) : false)
         return launch<256, 256, 2, 4, E>(g, stream);
     return launch<128, 128, 2, 2, E>(g, stream);
 }

@@ -705,6 +705,26 @@ __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *pa
     }
 }
 
+// The sum of `splits` rows' columns at p, `step` elements from each other, added in
+// their order, 8 loads at a time.
+template <int P>
+__device__ __forceinline__ Some<P> sum_of(const float *p, int64_t splits, int64_t step) {
+    Some<P> e{};
+    int64_t s = 0;
+    for (; s + 8 <= splits; s += 8) {
+        Some<P> v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = load_some<P, true>(p + (s + u) * step);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            add(e, v[u]);
+    }
+    for (; s < splits; ++s)
+        add(e, load_some<P, true>(p + s * step));
+    return e;
+}
+
 // The splits' sums of grad_hidden, added in their order, and the rest of the
 // target's d times its row; rounded. So the largest term of most sums is exact.
 // Bound by reading: 8,192 tokens of GPT-2 small, two splits, 13.5 us (50 MB of sums,
@@ -720,8 +740,7 @@ __global__ __launch_bounds__(256) void hidden_kernel(CeArgs a, const float *sum,
         Some<P> e{};
         if (target >= 0 && target < a.vocab) {
             const Some<P> w = load_some<P>(a.w + target * a.dim + c.at);
-            for (int64_t s = 0; s < splits; ++s)
-                add(e, load_some<P, true>(sum + (s * a.n + r) * kdim + c.at));
+            e = sum_of<P>(sum + r * kdim + c.at, splits, a.n * kdim);
             const float x = rest[r];
             for (int k = 0; k < P; ++k)
                 e.v[k] += x * w.v[k];
@@ -739,10 +758,7 @@ __global__ __launch_bounds__(256) void row_sums_kernel(RowsArgs r, const float *
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
         const int64_t row = i / per;
         const Columns<P> c(i % per * P, r.dim);
-        Some<P> e{};
-        for (int64_t s = 0; s < splits; ++s)
-            add(e, load_some<P, true>(sum + (s * rows + row) * kdim + c.at));
-        write_row<kAdd>(r, uint32_t(row), c, e);
+        write_row<kAdd>(r, uint32_t(row), c, sum_of<P>(sum + row * kdim + c.at, splits, rows * kdim));
     }
 }
 
@@ -756,21 +772,17 @@ void launch_pack(Pack one, Pack two, const CeArgs &a, const CeLayout &l, hipStre
         pack_kernel<<<unsigned(one.workgroups + two.workgroups), 256, 0, stream>>>(one, two, a.dim, l.kdim, a.vocab);
 }
 
-// W where it lies serves the products if its rows are whole steps and 16-byte
-// aligned; else they take a copy, piece by piece.
-bool in_place(const CeArgs &a) { return a.dim % kDepth == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0; }
-
 // Few tokens and W not in place: its rows are read as they lie by
 // thin_score_kernel rather than copied (16 tokens of Llama-3-8B, W off by an
 // element: 482 us, 660 with the copy; 10,007 rows of 1,537: 31 and 40. In place
 // the products are as fast: 184 and 182, GPT-2 small 23.5 and 21.8).
-bool by_rows(const CeArgs &a) { return a.n <= kThinTokens && !in_place(a); }
+bool by_rows(const CeArgs &a) { return a.n <= kThinTokens && !a.in_place; }
 
 // A piece of W as the products take it: in place, or the copy that `p` describes.
 const uint16_t *piece_of(const CeArgs &a, const CeLayout &l, int64_t row0, int64_t rows, Pack &p) {
     p = Pack{};
     const uint16_t *from = a.w + row0 * a.dim;
-    if (in_place(a))
+    if (a.in_place)
         return from;
     uint16_t *w = reinterpret_cast<uint16_t *>(a.workspace + l.w);
     p = Pack{from, a.dim, rows, rows, nullptr, w, 1, 0};
@@ -885,7 +897,7 @@ hipError_t launch_rows(const RowsArgs &a, hipStream_t stream) {
 hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return hipSuccess;
-    const CeLayout l = ce_layout(a.n, a.vocab, a.dim);
+    const CeLayout &l = a.layout;
     GemmArgs g{};
     g.b = a.hidden;
     g.ldb = a.n <= 1 ? a.dim : a.hidden_stride;
@@ -915,7 +927,7 @@ hipError_t launch_ce(const CeArgs &a, hipStream_t stream) {
         g.lda = l.kdim;   // dim where W is used in place
         g.k = l.kdim;
         // in place, W needs no pieces but for the tiles' numbers
-        const int64_t rows = in_place(a) ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
+        const int64_t rows = a.in_place ? std::max(l.piece, (int64_t(1) << 36) / l.npad / 256 * 256) : l.piece;
         for (g.row0 = 0; g.row0 < a.vocab; g.row0 += rows) {
             g.m = std::min(rows, a.vocab - g.row0);
             g.a = piece_of(a, l, g.row0, g.m, w);
@@ -944,7 +956,7 @@ hipError_t launch_ce_grad(const CeArgs &a, hipStream_t stream) {
     }
     if (a.n == 0)
         return hipSuccess;
-    const CeLayout l = ce_layout(a.n, a.vocab, a.dim);
+    const CeLayout &l = a.layout;
     auto u16 = [&](int64_t at) { return reinterpret_cast<uint16_t *>(a.workspace + at); };
     uint16_t *hidden = u16(l.hidden), *d = u16(l.d);
     float *sum = reinterpret_cast<float *>(a.workspace + l.sum);
