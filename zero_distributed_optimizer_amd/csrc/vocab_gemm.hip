@@ -363,13 +363,23 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
             constexpr bool kLow = BM == kTileRowsMin;
             uint16_t *mine = reinterpret_cast<uint16_t *>(stage) + epi_wave * (PM * PN);
             uint32_t packed[4];
+            // loads first (8,192 tokens of GPT-2 small 705 us, 693 so)
+            int64_t named_row[TN];
+            float lses[TN], weights[TN];
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int n = wave_n + j * 16 + lane_n;
-                const int64_t named_row = n < cols_in ? g.targets[n0 + n] : -1;
-                const bool named = named_row >= 0 && named_row < g.vocab;
-                const int target = row_of_target(g, named_row, m0 + wave_m, PM);
-                const float lse = named ? g.lse[n0 + n] : 0.0f, weight = named ? g.weight[n0 + n] : 0.0f;
+                const bool in = n < cols_in;
+                named_row[j] = in ? g.targets[n0 + n] : -1;
+                lses[j] = in ? g.lse[n0 + n] : 0.0f;
+                weights[j] = in ? g.weight[n0 + n] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int n = wave_n + j * 16 + lane_n;
+                const bool named = named_row[j] >= 0 && named_row[j] < g.vocab;
+                const int target = row_of_target(g, named_row[j], m0 + wave_m, PM);
+                const float lse = named ? lses[j] : 0.0f, weight = named ? weights[j] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
