@@ -19,7 +19,7 @@ struct Some {
     float v[P];
 };
 
-// kOnce: non-temporally, for what a launch reads once.
+// kOnce: non-temporally, for what a launch reads or writes once.
 template <bool kOnce, typename V>
 __device__ __forceinline__ V load_as(const void *p) {
     if constexpr (kOnce)
@@ -54,23 +54,31 @@ __device__ __forceinline__ Some<P> load_some(const float *p) {
         }
     return e;
 }
-template <int P>
+template <bool kOnce, typename V, typename X>
+__device__ __forceinline__ void store_as(void *p, const X &x) {
+    if constexpr (kOnce)
+        __builtin_nontemporal_store(V(x), static_cast<V *>(p));
+    else
+        *static_cast<V *>(p) = x;
+}
+
+template <bool kOnce = false, int P>
 __device__ __forceinline__ void store_some(uint16_t *p, const Some<P> &e) {
     if constexpr (P == 8)
-        *reinterpret_cast<loose_u32x4 *>(p) = u32x4{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3]),
-                                                  to_bf16x2(e.v[4], e.v[5]), to_bf16x2(e.v[6], e.v[7])};
+        store_as<kOnce, loose_u32x4>(p, u32x4{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3]),
+                                              to_bf16x2(e.v[4], e.v[5]), to_bf16x2(e.v[6], e.v[7])});
     else if constexpr (P == 4)
-        *reinterpret_cast<loose_u32x2 *>(p) = u32x2{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3])};
+        store_as<kOnce, loose_u32x2>(p, u32x2{to_bf16x2(e.v[0], e.v[1]), to_bf16x2(e.v[2], e.v[3])});
     else
         *p = uint16_t(to_bf16x2(e.v[0], 0.0f));
 }
-template <int P>
+template <bool kOnce = false, int P>
 __device__ __forceinline__ void store_some(float *p, const Some<P> &e) {
     if constexpr (P == 1)
         *p = e.v[0];
     else
         for (int i = 0; i < P; i += 4)
-            *reinterpret_cast<loose_f32x4 *>(p + i) = f32x4{e.v[i], e.v[i + 1], e.v[i + 2], e.v[i + 3]};
+            store_as<kOnce, loose_f32x4>(p + i, f32x4{e.v[i], e.v[i + 1], e.v[i + 2], e.v[i + 3]});
 }
 
 template <int P>
@@ -94,9 +102,12 @@ struct Columns {
 
 // ---- lookup ------------------------------------------------------------------------------
 // A wave takes kLookupChunks chunks of 64 lanes' columns of a row, all its
-// loads first. Bound by HBM: 16,384 rows of Llama-3-8B's 4,096 in bf16 34 us, 79 MB
-// read (tokens repeat) and 134 written, 6.2 TB/s; one token 2 us.
-constexpr int kLookupChunks = 2;
+// loads first; a lane writes 16 bytes at once (so in fp32 it takes 4 columns), and
+// non-temporally. Bound by HBM: 16,384 rows of Llama-3-8B's 4,096, W not in a cache,
+// to bf16 40.4 us (79 MB read, for tokens repeat, and 134 written: 5.3 TB/s; by
+// ordinary stores and half the loads 49.4), to fp32 72 us (84 by ordinary stores, 106
+// with two stores a lane); one token 2.3 us.
+constexpr int kLookupChunks = 4;
 
 template <typename T, int P>
 __global__ __launch_bounds__(256) void lookup_kernel(LookupArgs a) {
@@ -120,7 +131,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(LookupArgs a) {
                 for (float &v : e[k].v)
                     v = a.scale * v;
             if (c.any)
-                store_some(out + c.at, e[k]);
+                store_some<true>(out + c.at, e[k]);
         }
     }
 }
@@ -800,13 +811,13 @@ hipError_t launch_zero(uint16_t *p, int64_t n, hipStream_t stream) {
 hipError_t launch_lookup(const LookupArgs &a, hipStream_t stream) {
     if (a.n == 0)
         return hipSuccess;
-    const int P = a.dim >= 8 ? 8 : 1;
+    const int P = a.dim < 8 ? 1 : a.f32 ? 4 : 8;
     const dim3 grid(grid_of(ceil_div(a.n, 4)), unsigned(ceil_div(a.dim, 64 * P * kLookupChunks)));
     auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a); };
     if (a.f32)
-        P == 8 ? go(lookup_kernel<float, 8>) : go(lookup_kernel<float, 1>);
+        P == 1 ? go(lookup_kernel<float, 1>) : go(lookup_kernel<float, 4>);
     else
-        P == 8 ? go(lookup_kernel<uint16_t, 8>) : go(lookup_kernel<uint16_t, 1>);
+        P == 1 ? go(lookup_kernel<uint16_t, 1>) : go(lookup_kernel<uint16_t, 8>);
     return hipGetLastError();
 }
 
