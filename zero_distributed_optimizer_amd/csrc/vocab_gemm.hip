@@ -469,8 +469,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
         } else {
             // through LDS, in fp32, a wave's part [n][m] in as many passes as it
             // takes, so that rows are written by 16 bytes a lane and 256 or 128
-            // bytes on end (Llama-3-8B's matrix from 64 tokens 447 us, 511 straight from
-            // registers by 8 bytes; from 4,096 3.55 and 3.62 ms). Quads are moved within
+            // bytes on end (Llama-3-8B's matrix from 64 tokens 443 us, 511 straight from
+            // registers by 8 bytes; from 4,096 3.47 and 3.62 ms). Quads are moved within
             // their row by the row's number, so that the writes do not meet in a bank.
             constexpr int PM = BM / WM, PN = BN / WN, CM = PM / 8;
             constexpr int kPasses = BM * BN * 4 / int(sizeof(stage)), JN = TN / kPasses;
@@ -507,8 +507,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
                                 v[2 * r + 1] += hi_f32(old[r]);
                             }
                         }
-                        *to = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
-                                    to_bf16x2(v[6], v[7])};
+                        // non-temporally: W, hidden and d stay in the caches
+                        __builtin_nontemporal_store(u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]),
+                                                          to_bf16x2(v[4], v[5]), to_bf16x2(v[6], v[7])},
+                                                    to);
                     } else {
 #pragma unroll
                         for (int r = 0; r < 7; ++r)
