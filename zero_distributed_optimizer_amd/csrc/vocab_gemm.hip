@@ -173,11 +173,11 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-// Bound by the matrix cores and the power they draw (busy in 67 to 70% of the cycles,
-// at 1.85 to 1.9 of 2.4 GHz): Llama-3-8B, 4,096 tokens, the logits 3.05 ms (1,410
-// TFLOP/s), d 3.4, grad_hidden's sum 3.1, W's gradient 3.5 ms. With few steps a tile
+// Bound by the matrix cores and the power they draw (busy in 62 to 75% of the cycles,
+// at 1.85 to 1.9 of 2.4 GHz): Llama-3-8B, 4,096 tokens, the logits 3.0 ms (1,430
+// TFLOP/s), d 3.25, grad_hidden's sum 3.1, W's gradient 3.4 ms. With few steps a tile
 // the epilogues weigh, the cores idle meanwhile: GPT-2 small's 12, 8,192 tokens, the
-// logits 0.61 ms (1,040 TFLOP/s). Tiles of 256 x 256 read each operand from the caches
+// logits 0.58 ms (1,090 TFLOP/s). Tiles of 256 x 256 read each operand from the caches
 // half as often as those of 128 x 128, of which two share a compute unit.
 template <int BM, int BN, int WM, int WN, int E>
 __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
