@@ -444,6 +444,64 @@ def test_no_tokens(gpu):
         assert torch.equal(bits(g), bits(old))
 
 
+# ---- the largest sizes ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,dim,dtype", [((1 << 20) + 9, 3, BF), (1 << 20, 3, torch.float32), (513, 1 << 20, BF), (20, 1 << 20, BF)])
+def test_many_tokens_and_columns_of_rows(gpu, n, dim, dtype, accumulate):
+    test_embedding_grad(gpu, n, 40, dim, 1, 1, "zipf", 1.0, dtype, "contiguous", accumulate)
+
+
+def test_lookup_of_the_longest_rows(gpu):
+    test_lookup_is_exact(gpu, 3, 5, 1 << 20, 1, 0, "ends", 1.0, BF, "off")
+    test_lookup_is_exact(gpu, 3, 5, (1 << 20) - 1, 0, 0, "ends", 1.0, torch.float32, "contiguous")
+
+
+def test_cross_entropy_of_the_most_tokens(gpu):
+    check_ce(1 << 22, 17, 8, 0, 1, "uniform", "contiguous")
+
+
+@pytest.mark.parametrize("dim,before", [(1 << 20, 0), ((1 << 20) - 1, 1)])
+@pytest.mark.parametrize("n", [3, 40])
+def test_cross_entropy_of_the_longest_rows(gpu, n, dim, before):
+    """Rows of -1, 0 and 1 against rows of those over 512: every sum that a logit
+    is made of is a multiple of 1/512 below 2^11, so logits are exact."""
+    vocab = 3
+    plan, param, at = plan_for(before, vocab, dim)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    params = torch.randint(-1, 2, (plan.buffer_numel,), generator=gen, device=DEV).to(BF)
+    h = (torch.randint(-1, 2, (n, dim), generator=gen, device=DEV) / 512).to(BF)
+    w, targets = params[at].view(vocab, dim).double(), tokens_for(n, vocab, "uniform", 3)
+    weight = rand(n, seed=4, dtype=torch.float32)
+    z = h.double() @ w.t()
+    lse, named = torch.logsumexp(z, 1), (targets >= 0) & (targets < vocab)
+    hot = torch.nn.functional.one_hot(torch.where(named, targets, 0), vocab) * named[:, None]
+    loss_got, lse_got = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    gh, grads = torch.empty(n, dim, dtype=torch.float32, device=DEV), torch.zeros_like(params)
+    ws = ce_workspace(n, vocab, dim)
+    Z.linear_cross_entropy(plan, param, vocab, params, h, targets, loss_got, lse_got, ws)
+    Z.linear_cross_entropy_grad(plan, param, vocab, params, h, targets, lse_got, weight, gh, grads, ws)
+    # exponentials of differences up to x, each within (4 + 2x) units and joined
+    # three times, 67 additions of positive terms, a logarithm (4 units) and
+    # its addition: (12 + 6x + 67 + 4 + 2 + 2 |lse|) 2^-24 < 2^-17 (1 + x)
+    x = 2 * z.abs().amax(1) + 2
+    off = 2.0 ** -17 * (1 + x)
+    assert_within(lse_got, lse, off, "lse")
+    assert_within(loss_got, torch.where(named, lse - (z * hot).sum(1), 0.0), 2 * off, "loss")
+    weight = torch.where(named, weight.double(), 0.0)[:, None]
+    p = torch.exp(z - lse[:, None])
+    d = (p - hot) * weight
+    # p moves with lse, and has an exponential's error; one, the weight: a rounding each; bf16
+    dd = weight.abs() * (p * 3 * off[:, None] + 2 * U32 * (p + hot))
+    dd = dd + U16 * (d.abs() + dd) + TINY
+    size = d.abs() + dd
+    want, bound = d @ w, dd @ w.abs() + 8 * U32 * (size @ w.abs())
+    assert_within(gh, want, U32 * want.abs() + (1 + U32) * bound, "grad_hidden")
+    hn = torch.where(named[:, None], h.double(), 0.0)
+    want, bound = d.t() @ hn, dd.t() @ hn.abs() + (n + 8) * 2 * U32 * (size.t() @ hn.abs()) + TINY
+    assert_within(grads[at].view(vocab, dim), want, U16 * want.abs() + (1 + U16) * bound, "grads")
+
+
 # ---- the test build: 64 workgroups walk every launch ----------------------------------------------
 
 @pytest.mark.parametrize("n,vocab,dim,kind", [(3000, 5000, 40, "zipf"), (20000, 700, 24, "zipf"), (400, 9000, 1300, "zipf"),
