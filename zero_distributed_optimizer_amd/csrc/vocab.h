@@ -151,9 +151,9 @@ struct GemmArgs {
 // units take, kRoundK for each k of a round of large tiles (1.3 PFLOP/s) and
 // kRoundOwn of its own for each round, in us. A round of 512 small tiles has half
 // the work and takes 0.62 of a large one's time, of 256 and fewer 0.4 (loss of
-// 128 tokens of Llama-3-8B by small tiles 195 us, by large ones 238; 8,192 tokens
-// of GPT-2 small 778 and 646; the gradients of 16,384 tokens with this choice
-// 4.49 ms, at 0.5 and 0.3 4.61, at 1.1 and 0.9 5.00).
+// 128 tokens of Llama-3-8B by small tiles 197 us, by large ones 234; 8,192 tokens
+// of GPT-2 small 653 and 540; loss and gradients of those with this choice 2.44 ms,
+// at 0.5 and 0.3 2.63, at 1.1 and 0.9 2.51; of 16,384 tokens 5.04, 5.49 and 5.04).
 constexpr int kTileRowsMin = 128;
 constexpr double kRoundK = 0.026, kRoundOwn = 5.0;
 inline double wide_rounds(int64_t m, int64_t n, int64_t splits) {

@@ -694,7 +694,8 @@ hipError_t launch(const GemmArgs &g, hipStream_t stream) {
 
 template <int E>
 hipError_t launch_sized(const GemmArgs &g, hipStream_t stream) {
-    if (E != kDiff || !g.low ? wide_tiles(g.m, g.n, g.splits) : false)
+    const bool two_parts = E == kDiff && g.low;   // of few tokens: small tiles make them
+    if (!two_parts && wide_tiles(g.m, g.n, g.splits))
         return launch<256, 256, 2, 4, E>(g, stream);
     return launch<128, 128, 2, 2, E>(g, stream);
 }

@@ -785,7 +785,7 @@ void launch_pack(Pack one, Pack two, const CeArgs &a, const CeLayout &l, hipStre
 
 // Few tokens and W not in place: its rows are read as they lie by
 // thin_score_kernel rather than copied (16 tokens of Llama-3-8B, W off by an
-// element: 482 us, 660 with the copy; 10,007 rows of 1,537: 31 and 40. In place
+// element: 485 us, 648 with the copy; 10,007 rows of 1,537: 33 and 38. In place
 // the products are as fast: 184 and 182, GPT-2 small 23.5 and 21.8).
 bool by_rows(const CeArgs &a) { return a.n <= kThinTokens && !a.in_place; }
 
