@@ -89,7 +89,9 @@ int64_t zdo_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64
  *   lse_i  = log(sum over v < vocab of exp(z_i[v]))
  *   loss_i = lse_i - z_i[targets_i], 0 where the target names no row.
  * hidden: bf16. Products and sums in fp32, exponentials relative to a running
- * maximum. loss and lse: fp32, n elements each; lse is written for every
+ * maximum m_i; the loss is (m_i - z_i[targets_i]) + log(sum over v of exp(z_i[v] -
+ * m_i)), so that it is never negative and a small one keeps its digits however large
+ * the logits are. loss and lse: fp32, n elements each; lse is written for every
  * token. Outputs and workspace must not overlap the inputs or each other. */
 int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,
                          const uint16_t *params, const uint16_t *hidden, int64_t hidden_stride,

@@ -1,0 +1,47 @@
+"""GPU tests of the calls at the vocabulary matrix on inputs whose results are
+known to a few units of fp32, or to the last bit: what a bound that adds up the
+roundings of general inputs would hide."""
+
+import pytest
+import torch
+from test_gpu_vocab import BF, DEV, U32, assert_within, ce_workspace, plan_for
+
+import zero_distributed_optimizer_amd as Z
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- small losses of large logits ---------------------------------------------------------
+
+@pytest.mark.parametrize("n,vocab,dim,before", [(20, 300, 64, 0), (20, 300, 60, 3), (256, 300, 64, 0), (300, 1003, 64, 8),
+                                                (2049, 513, 64, 0)])
+def test_small_losses_of_large_logits(gpu, n, vocab, dim, before):
+    """The target's logit is 4096 and all others g below it, all exact, so that
+    loss = log(1 + (vocab - 1) exp(-g)) whatever the logits' size. Of that sum s the
+    exponentials are off by (4 + 2g) units (with their joins by no more than three
+    times that), the additions by 64 + vocab / 128 units of s; the logarithm by 2
+    units of itself and 1 / s of what s is off; with the last addition by 2 more.
+    Where the logarithm is rounded together with the largest logit, its error is up
+    to 2^-12 alone."""
+    plan, param, at = plan_for(before, vocab, dim)
+    params = torch.zeros(plan.buffer_numel, dtype=BF, device=DEV)
+    w = params[at].view(vocab, dim)
+    gap = (torch.arange(n, device=DEV) % 20 + 1).double()
+    targets = (torch.arange(n, device=DEV) * 7 + 3) % 5          # rows 0 to 4
+    # columns 0 to 4: which row is the target; 5: the gap; 6: what all rows share
+    w[:5, :5] = torch.eye(5, device=DEV).to(BF)
+    w[:, 5], w[:, 6] = -1.0, 64.0
+    h = torch.zeros(n, dim, dtype=BF, device=DEV)
+    h[torch.arange(n, device=DEV), targets] = gap.to(BF)
+    h[:, 5], h[:, 6] = gap.to(BF), 64.0
+    z = h.double() @ w.double().t()
+    assert torch.equal(z.amax(1), torch.full((n,), 4096.0, dtype=torch.float64, device=DEV))
+    want = torch.log1p((vocab - 1) * torch.exp(-gap))
+    off = ((4 + 2 * gap) * 3 + 64 + vocab / 128 + 4) * U32 * (1 + want)
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    Z.linear_cross_entropy(plan, param, vocab, params, h, targets, loss, lse, ce_workspace(n, vocab, dim))
+    assert_within(loss, want, off, "loss")
+    assert (loss >= 0).all()
+    assert_within(lse, 4096 + want, off + 2.0 ** -12, "lse")
+    # by way of lse in fp32 it would be beyond the bound
+    assert (((4096 + want).float().double() - 4096 - want).abs() > off).any()

@@ -707,10 +707,12 @@ __global__ __launch_bounds__(256) void combine_kernel(CeArgs a, const float2 *pa
         }
         if (slice == 0 && t < a.n) {
             all = red[0][token];
-            const float lse = all.x + logf(all.y);
+            // not by way of lse, where the largest logit's last bit may be more than the
+            // whole loss; with an infinite or NaN logit both ways give the same
+            const float log_sum = logf(all.y);
             const int64_t target = a.targets[t];
-            a.lse[t] = lse;
-            a.loss[t] = target >= 0 && target < a.vocab ? lse - pick[t] : 0.0f;
+            a.lse[t] = all.x + log_sum;
+            a.loss[t] = target >= 0 && target < a.vocab ? (all.x - pick[t]) + log_sum : 0.0f;
         }
         __syncthreads();
     }
