@@ -106,7 +106,8 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
  * the rounding leaves of d_i[targets_i], the largest term of most sums, is added
  * to grad_hidden in fp32, and for up to 128 tokens W's gradient takes d in two
  * bf16 parts. A token whose target names no row has a grad_hidden of zero.
- * grad_hidden or grads may be NULL (not both): that gradient is not computed.
+ * grad_hidden or grads may be NULL (both only with n = 0): that gradient is not
+ * computed.
  * hidden's rows of tokens whose target names no row are not used. Outputs
  * and workspace must not overlap the inputs or each other. */
 int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,

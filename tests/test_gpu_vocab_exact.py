@@ -45,3 +45,18 @@ def test_small_losses_of_large_logits(gpu, n, vocab, dim, before):
     assert_within(lse, 4096 + want, off + 2.0 ** -12, "lse")
     # by way of lse in fp32 it would be beyond the bound
     assert (((4096 + want).float().double() - 4096 - want).abs() > off).any()
+
+
+# ---- no tokens -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_the_gradient_by_hidden_of_no_tokens(gpu, dtype):
+    """An empty grad_hidden and no grads: nothing to do, and no error."""
+    vocab, dim = 40, 12
+    plan, param, at = plan_for(5, vocab, dim)
+    params = torch.ones(plan.buffer_numel, dtype=BF, device=DEV)
+    rows, f = torch.empty(0, dim, dtype=BF, device=DEV), torch.empty(0, device=DEV)
+    Z.linear_cross_entropy_grad(plan, param, vocab, params, rows, torch.empty(0, dtype=torch.int64, device=DEV), f,
+                                f.clone(), torch.empty(0, dim, dtype=dtype, device=DEV), None, ce_workspace(0, vocab, dim))
+    torch.cuda.synchronize()
+    assert (params == 1).all()

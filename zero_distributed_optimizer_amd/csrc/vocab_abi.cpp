@@ -272,7 +272,7 @@ int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t
             return rc;
         if (int rc = check_array(grad_loss, n, 4, fn, "grad_loss"))
             return rc;
-        if (!grad_hidden && !grads)
+        if (!grad_hidden && !grads && n > 0)   // with n = 0 an empty grad_hidden may be NULL
             return fail(ZDO_EINVAL, std::string(fn) + ": grad_hidden and grads are both NULL");
         if (grad_hidden) {
             if (int rc = check_type(grad_hidden_type, fn, "grad_hidden_type"))
