@@ -91,8 +91,30 @@ static int no_tokens() {
     return 0;
 }
 
+// What the header says of the workspace's parts: a piece's d (both parts of it) and
+// its copy of W take at most 256 MB each, or 256 rows of a piece for each token and
+// column; the sums of splits at most 128 MB for each gradient.
+static int documented_sizes() {
+    using namespace zdo;
+    std::mt19937_64 rng(5);
+    auto some = [&](double most) { return int64_t(std::pow(most, double(rng() % 100001) / 1e5)); };
+    constexpr int64_t kMB = 1 << 20, kRound = 256;   // parts are rounded up to 256 bytes
+    for (int t = 0; t < 4000; ++t) {
+        const int64_t n = t % 2 ? 1 + int64_t(rng() % 130) : some(double(kCeMaxN));
+        const int64_t vocab = some(double(kVocabMaxRows)), any = some(double(kVocabMaxDim));
+        const int64_t dim = t % 3 ? round_up(any, kDepth) : any;
+        const bool in_place = dim % kDepth == 0 && rng() % 2;
+        const CeLayout l = ce_layout(n, vocab, dim, in_place);
+        TRUE(l.rest - l.d <= std::max(256 * kMB, 512 * l.parts * l.npad) + kRound);
+        TRUE(in_place || l.d - l.w <= std::max(256 * kMB, 512 * l.kdim) + kRound);
+        TRUE(l.splits == 1 || l.row_sum - l.sum <= 128 * kMB + kRound);
+        TRUE(l.row_splits == 1 || 4 * l.row_splits * l.piece * l.kdim <= 128 * kMB);
+    }
+    return 0;
+}
+
 int main() {
-    if (no_tokens())
+    if (no_tokens() || documented_sizes())
         return 1;
     std::printf("ok: calls that the header allows\n");
     return 0;

@@ -211,11 +211,11 @@ inline bool rows_in_place(const void *w, int64_t dim) {
 }
 
 // A call's workspace. The vocabulary is taken in pieces of `piece` rows: at most
-// 2^27 elements of d (256 MB, the size of the Infinity Cache that they go
-// through to the two products that read them), but at least 256 rows, and, unless
-// W is read in place, at most 2^27 elements of its copy (Llama-3-8B in
-// place, by the smaller pieces: a training pass of 64 tokens 1.17 ms, 1.35; of 1,024
-// 3.94 and 4.12).
+// 2^27 elements of d, all its parts together (256 MB, the size of the Infinity
+// Cache that they go through to the two products that read them), but at least 256
+// rows, and, unless W is read in place, at most 2^27 elements of its copy
+// (Llama-3-8B in place, by the smaller pieces: a training pass of 64 tokens 1.17 ms,
+// 1.35; of 1,024 3.94 and 4.12).
 struct CeLayout {
     int64_t kdim, npad, piece, vpad;  // dim, n and piece up to a multiple of kDepth
     int64_t splits;                   // of grad_hidden's sum
@@ -229,7 +229,8 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim, bool in_place) 
     const int64_t some = std::max<int64_t>(n, 1);
     l.kdim = round_up(dim, kDepth);
     l.npad = round_up(some, kDepth);
-    int64_t most = (int64_t(1) << 27) / (in_place ? l.npad : std::max(l.npad, l.kdim));
+    l.parts = n <= kTwoPartTokens ? 2 : 1;
+    int64_t most = (int64_t(1) << 27) / (in_place ? l.parts * l.npad : std::max(l.parts * l.npad, l.kdim));
     most = std::max<int64_t>(256, most / 256 * 256);
     // the number of pieces, at least this many (few tokens: no more, their tiles
     // fill whole rounds anyway), and of splits of grad_hidden's sum over the
@@ -255,7 +256,6 @@ inline CeLayout ce_layout(int64_t n, int64_t vocab, int64_t dim, bool in_place) 
         at += round_up(bytes, 256);
         return here;
     };
-    l.parts = n <= kTwoPartTokens ? 2 : 1;
     l.hidden = take(2 * l.parts * l.npad * l.kdim);
     l.w = take(in_place ? 0 : 2 * l.piece * l.kdim);
     const int64_t both = at;
