@@ -29,6 +29,11 @@
  *     need their type's own alignment only; 16 bytes and strides of a multiple
  *     of 8 are fastest.
  *   - Types of activations: ZDO_BF16 or ZDO_F32.
+ *   - What a call writes must share no element with anything else of it. Rows may
+ *     lie between the rows of another array if both strides have as many bytes
+ *     (hidden and grad_hidden as two halves of one buffer's columns), and an array
+ *     without gaps between two rows; with strides that differ, arrays whose extents
+ *     meet are refused. What lies between rows is neither read nor written.
  *   - accumulate: 0 overwrites every element of the parameter in grads (those
  *     without a contribution become 0); otherwise the gradient is added to
  *     what is there, in fp32 and rounded once, and embedding_grad leaves rows

@@ -4,7 +4,7 @@ roundings of general inputs would hide."""
 
 import pytest
 import torch
-from test_gpu_vocab import BF, DEV, U32, assert_within, ce_workspace, plan_for
+from test_gpu_vocab import BF, DEV, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for
 
 import zero_distributed_optimizer_amd as Z
 
@@ -60,3 +60,38 @@ def test_the_gradient_by_hidden_of_no_tokens(gpu, dtype):
                                 f.clone(), torch.empty(0, dim, dtype=dtype, device=DEV), None, ce_workspace(0, vocab, dim))
     torch.cuda.synchronize()
     assert (params == 1).all()
+
+
+# ---- arrays between one another's rows ---------------------------------------------------------
+
+@pytest.mark.parametrize("n,vocab,dim,before,room", [(70, 300, 64, 0, 0), (300, 1003, 128, 8, 0), (20, 200, 60, 3, 4),
+                                                     (700, 500, 251, 1, 1), (2049, 513, 64, 0, 8)])
+def test_rows_between_rows(gpu, n, vocab, dim, before, room):
+    """hidden and grad_hidden as the two halves of one buffer's columns, the
+    tokens' x and its gradient too: the same bits as in buffers of their own, and
+    nothing else of the buffers is written."""
+    plan, param, at, params, w, targets, h, weight = ce_inputs(n, vocab, dim, before, 0, "zipf", "contiguous")
+    ws = torch.empty(max(Z.embedding_grad_workspace_bytes(n, dim), Z.linear_cross_entropy_workspace_bytes(n, vocab, dim)),
+                     dtype=torch.uint8, device=DEV)
+    wide = torch.full((n, 2 * (dim + room)), 7.0, dtype=BF, device=DEV)
+    left, right = wide[:, :dim], wide[:, dim + room:2 * dim + room]
+    results = []
+    for hidden, gh in ((h, torch.zeros_like(h)), (left, right), (right, left)):
+        wide.fill_(7.0)
+        hidden.copy_(h)
+        loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+        grads = torch.zeros_like(params)
+        Z.linear_cross_entropy(plan, param, vocab, params, hidden, targets, loss, lse, ws)
+        Z.linear_cross_entropy_grad(plan, param, vocab, params, hidden, targets, lse, weight, gh, grads, ws)
+        Z.embedding_grad(plan, param, vocab, targets, gh, grads, ws, accumulate=True)
+        results.append((loss, lse, gh.clone(), grads))
+        if gh._base is not None:
+            assert torch.equal(bits(hidden), bits(h))
+            Z.embedding_lookup(plan, param, vocab, params, targets, hidden)   # over hidden, beside its gradient
+            assert torch.equal(bits(gh), bits(results[-1][2]))
+            hidden.fill_(7.0)
+            gh.fill_(7.0)
+            assert (wide == 7.0).all()
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(bits(a), bits(b))

@@ -11,16 +11,45 @@
 
 namespace zdo {
 
+// The bytes [lo, hi) of an array; of rows with gaps between them those `width` bytes
+// that follow lo and every `step` bytes from it (step = 0: no gaps).
 struct Span {
-    uintptr_t lo, hi;
+    uintptr_t lo, hi, step, width;
 };
 
 inline Span span_of(const void *p, int64_t elems, int64_t elem_bytes) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + uintptr_t(elems) * uintptr_t(elem_bytes)};
+    return {lo, lo + uintptr_t(elems) * uintptr_t(elem_bytes), 0, 0};
 }
 
-inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+// n rows of dim elements, one every `stride` >= dim (of one row not looked at).
+inline Span span_of_rows(const void *p, int64_t n, int64_t dim, int64_t stride, int64_t elem_bytes) {
+    if (n <= 1)
+        return span_of(p, n == 1 ? dim : 0, elem_bytes);
+    Span s = span_of(p, (n - 1) * stride + dim, elem_bytes);
+    if (stride > dim) {
+        s.step = uintptr_t(stride * elem_bytes);
+        s.width = uintptr_t(dim * elem_bytes);
+    }
+    return s;
+}
+
+// Whether two arrays share a byte. Rows may lie in the gaps of rows whose step is the
+// same, and an array without gaps within one; with steps that differ, arrays whose
+// extents meet count as sharing.
+inline bool overlap(Span a, Span b) {
+    if (!(a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi))
+        return false;
+    if (a.step == b.step ? a.step == 0 : a.step && b.step)
+        return true;
+    const uintptr_t step = a.step ? a.step : b.step;
+    const uintptr_t wide_a = a.step ? a.width : a.hi - a.lo, wide_b = b.step ? b.width : b.hi - b.lo;
+    if (wide_a > step || wide_b > step - wide_a)
+        return true;
+    // where b's rows begin, from a's
+    const uintptr_t off = b.lo >= a.lo ? (b.lo - a.lo) % step : (step - (a.lo - b.lo) % step) % step;
+    return off < wide_a || off > step - wide_b;
+}
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

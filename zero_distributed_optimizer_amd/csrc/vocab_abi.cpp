@@ -95,10 +95,6 @@ CeArgs args_at(const uint16_t *w, int64_t vocab, int64_t dim, int64_t n) {
     return a;
 }
 
-Span span_of_rows(const void *p, int64_t n, int64_t dim, int64_t stride, int32_t type) {
-    return span_of(p, n == 0 ? 0 : n == 1 ? dim : (n - 1) * stride + dim, bytes_of(type));
-}
-
 }  // namespace
 }  // namespace zdo
 
@@ -129,7 +125,7 @@ int embedding_lookup(const zdo_plan *plan, int32_t param_index, int64_t vocab, i
         Buffers bufs;
         bufs.reads(span_of(params, plan->buffer_numel, 2), "params");
         bufs.reads(span_of(tokens, n, 8), "tokens");
-        bufs.writes(span_of_rows(out, n, dim, out_stride, out_type), "out");
+        bufs.writes(span_of_rows(out, n, dim, out_stride, bytes_of(out_type)), "out");
         if (int rc = bufs.check(fn))
             return rc;
         LookupArgs a{};
@@ -176,7 +172,7 @@ int embedding_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int
             return rc;
         Buffers bufs;
         bufs.reads(span_of(tokens, n, 8), "tokens");
-        bufs.reads(span_of_rows(grad_out, n, dim, grad_stride, grad_type), "grad_out");
+        bufs.reads(span_of_rows(grad_out, n, dim, grad_stride, bytes_of(grad_type)), "grad_out");
         bufs.writes(span_of(grads, plan->buffer_numel, 2), "grads");
         bufs.writes(span_of(workspace, rows_layout(n, dim).bytes, 1), "workspace");
         if (int rc = bufs.check(fn))
@@ -231,7 +227,7 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
         CeArgs a = args_at(params + w.start, vocab, dim, n);
         Buffers bufs;
         bufs.reads(span_of(params, plan->buffer_numel, 2), "params");
-        bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, ZDO_BF16), "hidden");
+        bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, bytes_of(ZDO_BF16)), "hidden");
         bufs.reads(span_of(targets, n, 8), "targets");
         bufs.writes(span_of(loss, n, 4), "loss");
         bufs.writes(span_of(lse, n, 4), "lse");
@@ -288,12 +284,12 @@ int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t
         CeArgs a = args_at(params + w.start, vocab, dim, n);
         Buffers bufs;
         bufs.reads(span_of(params, plan->buffer_numel, 2), "params");
-        bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, ZDO_BF16), "hidden");
+        bufs.reads(span_of_rows(hidden, n, dim, hidden_stride, bytes_of(ZDO_BF16)), "hidden");
         bufs.reads(span_of(targets, n, 8), "targets");
         bufs.reads(span_of(lse, n, 4), "lse");
         bufs.reads(span_of(grad_loss, n, 4), "grad_loss");
         if (grad_hidden)
-            bufs.writes(span_of_rows(grad_hidden, n, dim, grad_hidden_stride, grad_hidden_type), "grad_hidden");
+            bufs.writes(span_of_rows(grad_hidden, n, dim, grad_hidden_stride, bytes_of(grad_hidden_type)), "grad_hidden");
         if (grads)
             bufs.writes(span_of(grads, plan->buffer_numel, 2), "grads");
         bufs.writes(span_of(workspace, a.layout.bytes, 1), "workspace");
