@@ -30,16 +30,21 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 // 16 bytes a lane from base + its offset to LDS, lane after lane from `to` (the
 // same for the whole wave) on. Written as an instruction, because the compiler
 // would wait for all such copies before every LDS read (it cannot tell the slots
-// apart); the waits are wait_and_meet's. It has no result in registers, and
-// nothing else here uses m0.
+// apart); the waits are wait_and_meet's. It has no result in registers. m0, which
+// holds the place in LDS, is named as overwritten, so that no value of the
+// compiler's own is expected in it afterwards; the compiler warns that it would not
+// save the register, which is not asked of it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16_to_lds(const char *base, uint32_t offset, const uint16_t *to) {
     const uint32_t lds = __builtin_amdgcn_readfirstlane(
         uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint16_t *)to)));
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Where a target's row lies among `count` rows from the piece's row `from` on; -1
 // if it is none of them.
