@@ -4,7 +4,7 @@ roundings of general inputs would hide."""
 
 import pytest
 import torch
-from test_gpu_vocab import BF, DEV, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for
+from test_gpu_vocab import BF, DEV, TINY, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for, tokens_for
 
 import zero_distributed_optimizer_amd as Z
 
@@ -95,3 +95,97 @@ def test_rows_between_rows(gpu, n, vocab, dim, before, room):
     for other in results[1:]:
         for a, b in zip(results[0], other):
             assert torch.equal(bits(a), bits(b))
+
+
+# ---- sums that are whole numbers ------------------------------------------------------------------
+
+# n, vocab, dim, elements before W, and the form that the sizes get: pieces of the
+# vocabulary (a copy of W's rows each, or W in place) and the last one's rows, then
+# the tile and the splits of grad_hidden's sum and of W's gradient
+# (tests/test_vocab_forms_host.py holds the forms to the library's rules)
+WHOLE_CASES = [
+    (8403, 500, 1000, 3, "1 copied, last 500; sum 256/1, rows 128/6"),
+    (300, 8403, 1000, 3, "1 copied, last 8403; sum 128/9, rows 256/1"),
+    (513, 9687, 2601, 1, "1 copied, last 9687; sum 128/4, rows 256/1"),
+    (8403, 8403, 1000, 3, "1 copied, last 8403; sum 256/3, rows 256/3"),
+    (8403, 8403, 1024, 0, "1 in place, last 8403; sum 256/3, rows 256/3"),
+    (16001, 17001, 1000, 3, "3 copied, last 5225; sum 256/1, rows 256/2"),
+    (16001, 25001, 1024, 8, "5 in place, last 4521; sum 256/1, rows 256/3"),
+    (20001, 16500, 63, 1, "3 copied, last 5236; sum 128/3, rows 128/9"),
+    (100, 1100003, 64, 0, "3 in place, last 366307; sum 128/474, rows 128/1"),
+    (200, 17001, 16383, 1, "3 copied, last 5225; sum 128/2, rows 256/1"),
+    (4096, 33000, 2048, 0, "3 in place, last 10984; sum 256/2, rows 128/1"),
+]
+
+
+def whole_inputs(n, vocab, dim, before):
+    """Logits of 0 and -256: columns of one kind hold a -16 for a token, by its
+    class, and a 16 for the rows that its class is against. Of the others, one half
+    is a token's alone (-1, 0, 1) and one W's alone (-3 to 3)."""
+    gen = torch.Generator(device=DEV).manual_seed(n + 31 * vocab + dim)
+    draw = lambda lo, hi, *shape: torch.randint(lo, hi + 1, shape, generator=gen, device=DEV)   # noqa: E731
+    plan, param, at = plan_for(before, vocab, dim)
+    columns = torch.randperm(dim, generator=gen, device=DEV)
+    classes = min(8, dim // 4)
+    hidden_only, w_only = columns[classes:classes + dim // 3], columns[classes + dim // 3:]
+    kind, against = draw(0, classes - 1, n), draw(0, 1, vocab, classes)
+    h = torch.zeros(n, dim, dtype=BF, device=DEV)
+    h[torch.arange(n, device=DEV), columns[kind]] = -16.0
+    h[:, hidden_only] = draw(-1, 1, n, len(hidden_only)).to(BF)
+    params = torch.zeros(plan.buffer_numel, dtype=BF, device=DEV)
+    w = params[at].view(vocab, dim)
+    w[:, columns[:classes]] = 16.0 * against.to(BF)
+    w[:, w_only] = draw(-3, 3, vocab, len(w_only)).to(BF)
+    targets = draw(0, vocab - 1, n)
+    targets[draw(0, 15, n) == 0] = -100
+    weight = draw(1, 3 if n < 1 << 20 else 1, n).float()
+    return plan, param, at, params, w, h, kind, 1 - against, targets, weight
+
+
+@pytest.mark.parametrize("accumulate,dtype", [(False, BF), (True, torch.float32)])
+@pytest.mark.parametrize("n,vocab,dim,before,form", WHOLE_CASES)
+def test_sums_of_whole_numbers(gpu, n, vocab, dim, before, form, accumulate, dtype):
+    """With lse = 0, exponentials are 1 and 0 and d, its products and all their
+    sums (below 2^24, or multiples of 16 below 2^28) are whole numbers that fp32
+    holds: gradients are exact but for the last rounding. Where W's gradient is
+    added, what is there takes the sum away but for what its rounding to bf16 left,
+    so that one token or row too few or too many shows in the last digit."""
+    plan, param, at, params, w, h, kind, p, targets, weight = whole_inputs(n, vocab, dim, before)
+    named = targets >= 0
+    ws = ce_workspace(n, vocab, dim)
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    Z.linear_cross_entropy(plan, param, vocab, params, h, targets, loss, lse, ws)
+    count = p.sum(0).double()
+    assert (count > 0).all()
+    want, target = count.log()[kind], torch.where(named, targets, 0)
+    pick = -256.0 * (1 - p[target, kind]).double()
+    # a sum that is exact, its logarithm (2 units), and the additions to 0 and 256
+    assert_within(lse, want, 4 * U32 * want + TINY, "lse")
+    assert_within(loss, torch.where(named, want - pick, 0.0), 4 * U32 * (want + 256), "loss")
+
+    # sums over the vocabulary, by class; sums over the tokens, by class and by target
+    over_rows = p.double().t() @ w.double()
+    want_hidden = torch.where(named[:, None], weight.double()[:, None] * (over_rows[kind] - w[target].double()), 0.0)
+    by_class = torch.zeros(p.shape[1], dim, dtype=torch.float64, device=DEV)
+    by_target = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV)
+    for i in range(0, n, 1 << 20):
+        k = torch.arange(i, min(n, i + (1 << 20)), device=DEV)[named[i:i + (1 << 20)]]
+        x = weight[k].double()[:, None] * h[k].double()
+        by_class.index_add_(0, kind[k], x)
+        by_target.index_add_(0, targets[k], x)
+    want_rows = p.double() @ by_class - by_target
+    h[~named], weight[~named] = float("nan"), float("nan")
+    old = -want_rows.to(BF) if accumulate else torch.full_like(w, 7.0)
+    grads = torch.full_like(params, 5.0)
+    grads[at] = old.view(-1)
+    gh = torch.empty(n, dim, dtype=dtype, device=DEV)
+    ws.fill_(255)
+    Z.linear_cross_entropy_grad(plan, param, vocab, params, h, targets, torch.zeros_like(lse), weight, gh, grads, ws,
+                                accumulate=accumulate)
+    assert torch.equal(gh, want_hidden.to(dtype))
+    got = grads[at].view(vocab, dim)
+    assert torch.equal(got, ((want_rows + old.double()) if accumulate else want_rows).to(BF))
+    if accumulate:
+        assert (got.abs() <= 2.0 ** -8 * want_rows.abs()).all()
+    grads[at] = 5.0
+    assert (grads == 5.0).all()
