@@ -115,6 +115,9 @@ WHOLE_CASES = [
     (100, 1100003, 64, 0, "3 in place, last 366307; sum 128/474, rows 128/1"),
     (200, 17001, 16383, 1, "3 copied, last 5225; sum 128/2, rows 256/1"),
     (4096, 33000, 2048, 0, "3 in place, last 10984; sum 256/2, rows 128/1"),
+    # the most tokens
+    (1 << 22, 40, 24, 8, "1 copied, last 40; sum 128/1, rows 128/474"),
+    ((1 << 22) - 1, 17, 8, 0, "1 copied, last 17; sum 128/1, rows 128/474"),
 ]
 
 
@@ -187,5 +190,38 @@ def test_sums_of_whole_numbers(gpu, n, vocab, dim, before, form, accumulate, dty
     assert torch.equal(got, ((want_rows + old.double()) if accumulate else want_rows).to(BF))
     if accumulate:
         assert (got.abs() <= 2.0 ** -8 * want_rows.abs()).all()
+    grads[at] = 5.0
+    assert (grads == 5.0).all()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab,dim,before,kind,dtype", [
+    ((1 << 20) + 9, 40, 3, 1, "zipf", BF),
+    (1 << 20, 40, 3, 1, "one", torch.float32),
+    ((1 << 22) + 1, 1000, 8, 0, "zipf", BF),
+    ((1 << 22) + 1, 2, 9, 3, "uniform", torch.float32),
+    (300000, 7, 1030, 8, "zipf", torch.float32),
+    (8192, 3, 2051, 3, "one", BF),
+    (512, 3, 72, 0, "one", BF),
+])
+def test_embedding_grad_of_whole_numbers(gpu, n, vocab, dim, before, kind, dtype, accumulate):
+    """Rows of -1, 0 and 1: every sum is exact, as in the test above."""
+    plan, param, at = plan_for(before, vocab, dim)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.randint(-1, 2, (n, dim), generator=gen, device=DEV).to(dtype)
+    tokens = tokens_for(n, vocab, kind, 5)
+    named = (tokens >= 0) & (tokens < vocab)
+    want = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV)
+    for i in range(0, n, 1 << 20):
+        k = slice(i, i + (1 << 20))
+        want.index_add_(0, torch.where(named[k], tokens[k], 0), torch.where(named[k, None], x[k].double(), 0.0) * 2.0)
+    x[~named] = float("nan")
+    old = -want.to(BF) if accumulate else torch.full((vocab, dim), 7.0, dtype=BF, device=DEV)
+    grads = torch.full((plan.buffer_numel,), 5.0, dtype=BF, device=DEV)
+    grads[at] = old.view(-1)
+    ws = torch.full((Z.embedding_grad_workspace_bytes(n, dim),), 255, dtype=torch.uint8, device=DEV)
+    Z.embedding_grad(plan, param, vocab, tokens, x, grads, ws, scale=2.0, accumulate=accumulate)
+    got = grads[at].view(vocab, dim)
+    assert torch.equal(got, ((want + old.double()) if accumulate else want).to(BF))
     grads[at] = 5.0
     assert (grads == 5.0).all()
