@@ -4,7 +4,8 @@ roundings of general inputs would hide."""
 
 import pytest
 import torch
-from test_gpu_vocab import BF, DEV, TINY, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for, tokens_for
+from test_gpu_vocab import (BF, DEV, TINY, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for, rand,
+                            tokens_for)
 
 import zero_distributed_optimizer_amd as Z
 
@@ -225,3 +226,74 @@ def test_embedding_grad_of_whole_numbers(gpu, n, vocab, dim, before, kind, dtype
     assert torch.equal(got, ((want + old.double()) if accumulate else want).to(BF))
     grads[at] = 5.0
     assert (grads == 5.0).all()
+
+
+# ---- what d's rounding leaves ------------------------------------------------------------------------
+
+def bf16_of(x):
+    return x.to(BF).double()
+
+
+@pytest.mark.parametrize("n,vocab,dim,before", [(1, 7, 9, 0), (33, 700, 100, 1), (100, 700, 64, 0), (129, 300, 64, 8),
+                                                (300, 1003, 251, 13), (2100, 5001, 65, 3), (9000, 9000, 192, 0),
+                                                (20001, 16500, 63, 1)])
+def test_the_rest_of_the_targets_d(gpu, n, vocab, dim, before):
+    """With hidden = 0 and lse = 300 every exponential is 0, d has the target's
+    -weight alone, and grad_hidden is -weight * W[target]: of d's bf16 part an exact
+    product, of the rest a product and an addition in fp32. Without the rest it would
+    be off by up to 2^-9 of itself."""
+    plan, param, at = plan_for(before, vocab, dim)
+    params = rand(plan.buffer_numel, seed=1)
+    w = params[at].view(vocab, dim)
+    h, targets = torch.zeros(n, dim, dtype=BF, device=DEV), tokens_for(n, vocab, "zipf", 2)
+    weight = rand(n, seed=3, dtype=torch.float32)
+    gh = torch.empty(n, dim, device=DEV)
+    for grads in (None, torch.zeros_like(params)):
+        gh.fill_(7.0)
+        Z.linear_cross_entropy_grad(plan, param, vocab, params, h, targets, torch.full((n,), 300.0, device=DEV), weight,
+                                    gh, grads, ce_workspace(n, vocab, dim))
+        named = ((targets >= 0) & (targets < vocab))[:, None]
+        rows = w[torch.where(named[:, 0], targets, 0)].double()
+        want = torch.where(named, -weight.double()[:, None] * rows, 0.0)
+        assert_within(gh, want, 2 * U32 * want.abs(), "grad_hidden")
+        coarse = torch.where(named, -bf16_of(weight)[:, None] * rows, 0.0)
+        assert ((coarse - want).abs() > 2 * U32 * want.abs())[named[:, 0]].float().mean() > 0.9 or n == 1
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab,dim,before", [(2, 5, 8, 0), (50, 60, 60, 3), (64, 300, 64, 0), (127, 64, 128, 8),
+                                                (128, 700, 251, 1), (128, 1100003, 64, 0)])
+def test_ds_two_parts_for_few_tokens(gpu, n, vocab, dim, before, accumulate):
+    """As above, and tokens in pairs with the same target and hidden state (whole
+    numbers), of weights a and -b in [1, 2) with 16 digits: two bf16 parts hold them,
+    and the row's sum (b - a) * hidden is exact. By one part each, a and b are off by
+    up to 2^-8, as much as their difference may be."""
+    plan, param, at = plan_for(before, vocab, dim)
+    gen = torch.Generator(device=DEV).manual_seed(n + vocab)
+    params = torch.zeros(plan.buffer_numel, dtype=BF, device=DEV)
+    pairs = n // 2
+    pair = torch.randperm(vocab, generator=gen, device=DEV)[:pairs]
+    order = torch.randperm(n, generator=gen, device=DEV)   # an odd one names nothing
+    targets = torch.cat([pair, pair, pair.new_full((n - 2 * pairs,), -1)])[order]
+    row_h = torch.randint(-7, 8, (pairs, dim), generator=gen, device=DEV).double()
+    h = torch.cat([row_h, row_h, row_h.new_full((n - 2 * pairs, dim), float("nan"))])[order].to(BF)
+    a, b = (1 + torch.randint(0, 1 << 15, (2, pairs), generator=gen, device=DEV).double() / (1 << 15)).unbind(0)
+    weight = torch.cat([a, -b, a.new_full((n - 2 * pairs,), float("nan"))])[order].float()
+
+    def total(x, y):
+        rows = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV)
+        rows[pair] = (y - x)[:, None] * row_h
+        return rows
+
+    want = total(a, b)
+    old = -want.to(BF) if accumulate else torch.full((vocab, dim), 7.0, dtype=BF, device=DEV)
+    grads = torch.full_like(params, 5.0)
+    grads[at] = old.view(-1)
+    for gh in (None, torch.empty(n, dim, dtype=BF, device=DEV)):
+        out = grads.clone()
+        Z.linear_cross_entropy_grad(plan, param, vocab, params, h, targets, torch.full((n,), 300.0, device=DEV), weight,
+                                    gh, out, ce_workspace(n, vocab, dim), accumulate=accumulate)
+        result = ((want + old.double()) if accumulate else want).to(BF)
+        assert torch.equal(out[at].view(vocab, dim), result)
+    coarse = total(bf16_of(a), bf16_of(b)).to(BF)
+    assert (coarse != want.to(BF))[pair].float().mean() > 0.5
