@@ -5,7 +5,7 @@ roundings of general inputs would hide."""
 import pytest
 import torch
 from test_gpu_vocab import (BF, DEV, TINY, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for, rand,
-                            tokens_for)
+                            step_of, tokens_for)
 
 import zero_distributed_optimizer_amd as Z
 
@@ -297,3 +297,31 @@ def test_ds_two_parts_for_few_tokens(gpu, n, vocab, dim, before, accumulate):
         assert torch.equal(out[at].view(vocab, dim), result)
     coarse = total(bf16_of(a), bf16_of(b)).to(BF)
     assert (coarse != want.to(BF))[pair].float().mean() > 0.5
+
+
+# ---- two streams ------------------------------------------------------------------------------------------
+
+def test_two_streams_write_all_of_w_gradient(gpu):
+    """Two steps at once on two streams, W's gradient (and every other output)
+    filled with NaN before each round: what a call left unwritten shows."""
+    sizes = [(2000, 3000, 192), (9000, 2000, 64)]
+    steps = [step_of(*s, seed=40 + i) for i, s in enumerate(sizes)]
+    slices = [slice(8, 8 + vocab * dim) for _, vocab, dim in sizes]
+    want = []
+    for run, out, _ in steps:
+        run()
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in out.items()})
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(4):
+        for (_, out, _), at in zip(steps, slices):
+            for k, v in out.items():
+                (v[at] if k == "grads" else v).fill_(float("nan"))
+        torch.cuda.synchronize()
+        for (run, _, _), stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                run()
+        torch.cuda.synchronize()
+        for (_, out, _), ref in zip(steps, want):
+            for k, v in out.items():
+                assert torch.equal(bits(v), bits(ref[k])), k
