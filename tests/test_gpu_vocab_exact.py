@@ -325,3 +325,29 @@ def test_two_streams_write_all_of_w_gradient(gpu):
         for (_, out, _), ref in zip(steps, want):
             for k, v in out.items():
                 assert torch.equal(bits(v), bits(ref[k])), k
+
+
+# ---- rows far from each other, and a workspace of 16-byte alignment --------------------------------------
+
+@pytest.mark.parametrize("n,vocab,dim,before,stride", [(3, 300, 64, 0, 1 << 30), (3, 300, 60, 3, (1 << 30) - 1),
+                                                       (300, 700, 64, 8, 1 << 21), (300, 700, 64, 8, (1 << 21) + 8),
+                                                       (520, 700, 70, 0, 1 << 22)])
+def test_rows_far_apart(gpu, n, vocab, dim, before, stride):
+    """Activations' rows at strides up to the largest, some of them beyond 2^32
+    bytes: the same bits as from rows that follow each other."""
+    plan, param, at, params, w, targets, h, weight = ce_inputs(n, vocab, dim, before, 0, "zipf", "contiguous")
+    need = max(Z.embedding_grad_workspace_bytes(n, dim), Z.linear_cross_entropy_workspace_bytes(n, vocab, dim))
+    far = [torch.zeros((n - 1) * stride + dim, dtype=BF, device=DEV).as_strided((n, dim), (stride, 1)) for _ in range(2)]
+    results = []
+    for hidden, gh, off in ((h, torch.empty_like(h), 0), (*far, 16)):
+        ws = torch.full((need + off,), 255, dtype=torch.uint8, device=DEV)[off:]
+        hidden.copy_(h)
+        loss, lse, grads = torch.empty(n, device=DEV), torch.empty(n, device=DEV), torch.zeros_like(params)
+        Z.linear_cross_entropy(plan, param, vocab, params, hidden, targets, loss, lse, ws)
+        Z.linear_cross_entropy_grad(plan, param, vocab, params, hidden, targets, lse, weight, gh, grads, ws)
+        gx = gh.clone()
+        Z.embedding_grad(plan, param, vocab, targets, gh, grads, ws, accumulate=True)
+        Z.embedding_lookup(plan, param, vocab, params, targets, gh, scale=3.0)
+        results.append((loss, lse, gx.contiguous(), grads, gh.contiguous()))
+    for a, b in zip(*results):
+        assert torch.equal(bits(a), bits(b))
