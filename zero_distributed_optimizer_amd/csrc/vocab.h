@@ -36,7 +36,9 @@ struct LookupArgs {
 // Sorted positions that a wave sums (see runs_kernel): at most its 64 lanes;
 // with few positions fewer each, so that the chip has waves enough (8,192
 // tokens of GPT-2 small: 8.4 us by 8, 11.6 by 16, 19 by 32; 131,072: the sums
-// take the same at 16 and 64, and joining the parts 39 us at 16, 13 at 64).
+// take the same at 16 and 64, and joining the parts 39 us at 16, 13 at 64). Rows of
+// more columns make more waves, which the rule does not look at: 8,192 tokens of
+// Llama-3-8B spend 19 of 233 us in joining, most workgroups finding nothing to join.
 inline int rows_chunk(int64_t n) { return n >= 65536 ? 64 : n >= 32768 ? 32 : n >= 16384 ? 16 : 8; }
 
 struct RowsArgs {
@@ -58,8 +60,9 @@ struct RowsArgs {
 constexpr int64_t kFewTokens = 512;
 
 // Up to this many positions are sorted by counting, in one launch (see
-// rank_kernel); more by digits (GPT-2 small: 8,192 tokens 33 us, by digits 50;
-// 16,384 by digits 52, by counting 56).
+// rank_kernel, which holds as many keys in 32 KB of LDS); more by digits (GPT-2 small:
+// 8,192 tokens 33 us, by digits 50; 16,384 by digits 52, by counting 56, so that they
+// would cross a little below that).
 constexpr int64_t kRankMax = 8192;
 // Sorting by digits: positions a workgroup takes (few, so that there are
 // workgroups enough; more where the scan of a digit's counts would weigh: of 50,257

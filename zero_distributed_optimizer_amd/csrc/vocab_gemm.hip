@@ -179,10 +179,11 @@ __device__ __forceinline__ void wait_and_meet() {
 }
 
 // Bound by the matrix cores and the power they draw (busy in 62 to 75% of the cycles,
-// at 1.85 to 1.9 of 2.4 GHz): Llama-3-8B, 4,096 tokens, the logits 3.0 ms (1,430
-// TFLOP/s), d 3.25, grad_hidden's sum 3.1, W's gradient 3.4 ms. With few steps a tile
-// the epilogues weigh, the cores idle meanwhile: GPT-2 small's 12, 8,192 tokens, the
-// logits 0.58 ms (1,090 TFLOP/s). Tiles of 256 x 256 read each operand from the caches
+// at 1.85 to 1.9 of 2.4 GHz): Llama-3-8B, 4,096 tokens, the logits 2.91 ms (1,480
+// TFLOP/s), d 3.11, grad_hidden's sum 3.00, W's gradient 3.28 ms (medians; a call's
+// first passes are up to 15% longer, until the clock has settled). With few steps a
+// tile the epilogues weigh, the cores idle meanwhile: GPT-2 small's 12, 8,192 tokens,
+// the logits 0.56 ms (1,130 TFLOP/s). Tiles of 256 x 256 read each operand from the caches
 // half as often as those of 128 x 128, of which two share a compute unit.
 template <int BM, int BN, int WM, int WN, int E>
 __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
@@ -533,8 +534,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_kernel(GemmArgs g) {
 // reads W from memory to registers as the instruction takes it (lane l: 16 bytes
 // of row l % 16), the next 64 k while it multiplies these. Rows start anywhere
 // and have any length; hidden comes out of the caches. The quarters are added
-// through LDS. Bound by reading W in rows off 16 bytes: 16 tokens of Llama-3-8B, off
-// by an element, 1.05 GB in 482 us.
+// through LDS. Bound by the L1 caches' address units, busy in 84% of the cycles: a lane's
+// 16 bytes off their alignment count as 3.5 accesses of the cache on average (16 tokens of
+// Llama-3-8B, off by an element: 1.05 GB in 482 us and 287 M accesses, where W in place
+// takes 182 us and 33 M by copies of aligned 16 bytes).
 template <int TN>
 __global__ __launch_bounds__(256, 2) void thin_score_kernel(GemmArgs g) {
     constexpr int TM = kThinRows / 16;
