@@ -113,7 +113,8 @@ int linear_cross_entropy(const zdo_plan *plan, int32_t param_index, int64_t voca
  * bf16 parts. A token whose target names no row has a grad_hidden of zero.
  * grad_hidden or grads may be NULL (both only with n = 0): that gradient is not
  * computed.
- * hidden's rows of tokens whose target names no row are not used. Outputs
+ * hidden's rows of tokens whose target names no row are not used. An infinite
+ * element of W leaves no finite number in its column of grad_hidden. Outputs
  * and workspace must not overlap the inputs or each other. */
 int linear_cross_entropy_grad(const zdo_plan *plan, int32_t param_index, int64_t vocab, int64_t dim,
                               const uint16_t *params, const uint16_t *hidden, int64_t hidden_stride,

@@ -2,10 +2,11 @@
 known to a few units of fp32, or to the last bit: what a bound that adds up the
 roundings of general inputs would hide."""
 
+import numpy as np
 import pytest
 import torch
-from test_gpu_vocab import (BF, DEV, TINY, U32, assert_within, bits, ce_inputs, ce_workspace, plan_for, rand,
-                            step_of, tokens_for)
+from test_gpu_vocab import (BF, DEV, TINY, U32, Reference, assert_within, bits, ce_inputs, ce_workspace, plan_for,
+                            rand, step_of, tokens_for)
 
 import zero_distributed_optimizer_amd as Z
 
@@ -351,3 +352,77 @@ def test_rows_far_apart(gpu, n, vocab, dim, before, stride):
         results.append((loss, lse, gx.contiguous(), grads, gh.contiguous()))
     for a, b in zip(*results):
         assert torch.equal(bits(a), bits(b))
+
+
+# ---- every bf16 number, and Inf and NaN in a token's gradient --------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("scale", [1.0, 0.5, 2.0 ** -9, 3.0, 2.0 ** 127, -1.0, 0.0, float("inf")])
+def test_lookup_of_every_bf16_number(gpu, scale, dtype):
+    """Subnormal numbers, zeros of both signs, infinities and NaN among them: one
+    fp32 product, rounded once."""
+    vocab, dim = 512, 128
+    plan, param, at = plan_for(8, vocab, dim)
+    params = torch.zeros(plan.buffer_numel, dtype=BF, device=DEV)
+    params[at] = torch.arange(-(1 << 15), 1 << 15, device=DEV).to(torch.int16).view(BF)
+    tokens = torch.randperm(vocab, device=DEV)
+    out = torch.empty(vocab, dim, dtype=dtype, device=DEV)
+    Z.embedding_lookup(plan, param, vocab, params, tokens, out, scale=scale)
+    # on the host, where no product or rounding takes subnormal numbers for zero
+    w = params[at].view(vocab, dim).cpu()[tokens.cpu()].float().numpy()
+    with np.errstate(all="ignore"):
+        want = torch.from_numpy(w * np.float32(scale)).to(dtype)
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(out.cpu()), nan)
+    assert torch.equal(bits(out.cpu())[~nan], bits(want)[~nan])
+
+
+@pytest.mark.parametrize("n", [40, 600, 9000])
+def test_a_poisoned_gradient_stays_in_its_row(gpu, n):
+    """Inf and NaN in one token's grad_out reach the elements of its token's row
+    that they stand at, and nothing else."""
+    vocab, dim = 300, 72
+    plan, param, at = plan_for(3, vocab, dim)
+    x, tokens = rand(n, dim, seed=1), tokens_for(n, vocab, "zipf", 2)
+    tokens[5] = 7
+    ws = torch.empty(Z.embedding_grad_workspace_bytes(n, dim), dtype=torch.uint8, device=DEV)
+    results = []
+    for poison in (False, True):
+        if poison:
+            x[5, 3], x[5, 64], x[5, 71] = float("inf"), float("nan"), float("-inf")
+        grads = torch.ones(plan.buffer_numel, dtype=BF, device=DEV)
+        Z.embedding_grad(plan, param, vocab, tokens, x, grads, ws, accumulate=True)
+        results.append(grads)
+    row = results[1][at].view(vocab, dim)[7]
+    assert row[3] == float("inf") and torch.isnan(row[64]) and row[71] == float("-inf")
+    row[[3, 64, 71]] = results[0][at].view(vocab, dim)[7, [3, 64, 71]]
+    assert torch.equal(bits(results[1]), bits(results[0]))
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("n,vocab,dim,before,row", [(100, 300, 64, 0, 5), (100, 300, 64, 0, 299), (600, 301, 72, 3, 300),
+                                                    (9000, 9000, 192, 0, 8999)])
+def test_a_poisoned_row_of_w_stays_in_its_column(gpu, n, vocab, dim, before, row, value):
+    """An infinite logit of minus infinity has no weight: losses of other targets
+    stay as they are without that row, and grad_hidden is not finite in the column
+    only where the infinity stands (0 times it), as the formula has it. A NaN reaches
+    every token's loss."""
+    plan, param, at, params, w, targets, h, weight = ce_inputs(n, vocab, dim, before, 0, "uniform", "contiguous")
+    h[:, 3] = -1.0
+    w[row, 3] = value
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    gh, grads = torch.empty(n, dim, device=DEV), torch.zeros_like(params)
+    ws = ce_workspace(n, vocab, dim)
+    Z.linear_cross_entropy(plan, param, vocab, params, h, targets, loss, lse, ws)
+    if value != value:
+        assert torch.isnan(loss).all() and torch.isnan(lse).all()
+        return
+    hits = targets == row
+    assert torch.isfinite(lse).all() and torch.isfinite(loss[~hits]).all() and (loss[hits] == value).all()
+    # the row adds an exact 0
+    ref = Reference(torch.cat([w[:row], w[row + 1:]]), h, torch.zeros_like(targets), weight, vocab - 1)
+    assert_within(lse, ref.lse, ref.d_lse, "lse")
+    Z.linear_cross_entropy_grad(plan, param, vocab, params, h, targets, lse, weight, gh, grads, ws)
+    assert not torch.isfinite(gh[:, 3]).any()
+    others = torch.arange(dim, device=DEV) != 3
+    assert torch.isfinite(gh[:, others]).all() and torch.isfinite(grads.float()).all()
