@@ -242,7 +242,7 @@ def test_the_rest_of_the_targets_d(gpu, n, vocab, dim, before):
     """With hidden = 0 and lse = 300 every exponential is 0, d has the target's
     -weight alone, and grad_hidden is -weight * W[target]: of d's bf16 part an exact
     product, of the rest a product and an addition in fp32. Without the rest it would
-    be off by up to 2^-9 of itself."""
+    be off by up to 2^-8 of itself."""
     plan, param, at = plan_for(before, vocab, dim)
     params = rand(plan.buffer_numel, seed=1)
     w = params[at].view(vocab, dim)
